@@ -30,7 +30,9 @@ EXPORTS = ("scope_workspace_bytes", "scope_cluster_queries", "scope_cluster_keys
            "scope_selection_recall", "scope_permute_channels", "scope_dense_attention",
            "scope_rope3d", "scope_layer_is_dense", "scope_attention_layer",
            "scope_rank_correlation_scratch_bytes", "scope_rank_correlation", "scope_check_wait_timeout",
-           "scope_tc_accumulation_probe")
+           "scope_tc_accumulation_probe",
+           "scope_qk_norm_workspace_bytes", "scope_qk_norm_rope3d", "scope_qk_norm_rope3d_backward",
+           "scope_window_workspace_bytes", "scope_window_attention", "scope_window_attention_backward")
 
 
 class ScopeError(RuntimeError):
@@ -75,6 +77,30 @@ class Schedule(ctypes.Structure):
     schedule (dense when layer < dense_layers or step < dense_steps)."""
     _fields_ = [("layer", ctypes.c_int), ("step", ctypes.c_int), ("dense_layers", ctypes.c_int),
                 ("dense_steps", ctypes.c_int), ("rope", ctypes.c_int), ("rope_base", ctypes.c_double)]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "head", "token")]
+
+
+class QkNormParams(ctypes.Structure):
+    """scope_qk_norm_params: shape, channel split and positions of a query/key norm with RoPE."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "Hkv", "N", "d", "d_t", "d_h", "d_w", "Hg", "Wg", "first")] + \
+               [("eps", ctypes.c_double), ("base", ctypes.c_double), ("dtype", ctypes.c_int)]
+
+
+class QkNormLayouts(ctypes.Structure):
+    _fields_ = [(n, Strides) for n in ("q", "k", "yq", "yk", "dq", "dk")]
+
+
+class WindowParams(ctypes.Structure):
+    """scope_window_params: shape and window (in frames) of a windowed attention."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "Hkv", "Nq", "Nk", "d", "frame", "left", "right", "sinks",
+                                            "q_first", "dtype")]
+
+
+class WindowLayouts(ctypes.Structure):
+    _fields_ = [(n, Strides) for n in ("q", "k", "v", "o", "d_o", "dq", "dk", "dv")]
 
 
 class Intermediates(ctypes.Structure):
@@ -138,6 +164,19 @@ def lib() -> ctypes.CDLL:
         L.scope_check_wait_timeout.argtypes = [P, ctypes.c_uint64, vp, sz, vp]
         L.scope_tc_accumulation_probe.restype = i
         L.scope_tc_accumulation_probe.argtypes = [vp, vp, i, i, vp, vp]
+        # struct pointers as plain pointers: a ctypes.byref costs less to pass than a typed one
+        L.scope_qk_norm_workspace_bytes.restype = sz
+        L.scope_qk_norm_workspace_bytes.argtypes = [vp]
+        L.scope_qk_norm_rope3d.restype = i
+        L.scope_qk_norm_rope3d.argtypes = [vp] * 10
+        L.scope_qk_norm_rope3d_backward.restype = i
+        L.scope_qk_norm_rope3d_backward.argtypes = [vp] * 14 + [sz, vp]
+        L.scope_window_workspace_bytes.restype = sz
+        L.scope_window_workspace_bytes.argtypes = [vp]
+        L.scope_window_attention.restype = i
+        L.scope_window_attention.argtypes = [vp] * 10 + [sz, vp]
+        L.scope_window_attention_backward.restype = i
+        L.scope_window_attention_backward.argtypes = [vp] * 14 + [sz, vp]
         _lib = L
     return _lib
 
@@ -361,6 +400,169 @@ def attention_layer(p, sched: Schedule, Q, K, V, q_init_idx=None, k_init_idx=Non
         ctypes.byref(p), ctypes.byref(sched), _ptr(Q), _ptr(K), _ptr(V), _ptr(q_init_idx), _ptr(k_init_idx),
         _ptr(O), _ptr(Qr), _ptr(Kr), _ptr(ws), ws.numel(), _stream(stream)))
     return O
+
+
+def _tensors(fn, p, layouts, named):
+    """The layouts argument of a strided call (None when every tensor is dense), after a check
+    of each (name, tensor, shape): device, type, shape and contiguous channels."""
+    dt = torch.bfloat16 if p.dtype == SCOPE_BF16 else torch.float32
+    dev, lay = named[0][1].device, None
+    for name, t, shape in named:
+        if t.shape != shape or t.dtype != dt or t.device != dev or not t.is_cuda:
+            raise ValueError(f"{fn}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, wanted {shape} {dt} on {dev}")
+        if not t.is_contiguous():
+            st = t.stride()
+            if st[3] != 1:
+                raise ValueError(f"{fn}: the channels of {name} are not contiguous (strides {st})")
+            lay = layouts() if lay is None else lay
+            setattr(lay, name, Strides(st[0], st[1], st[2]))
+    return lay
+
+
+def _vector(fn, name, t, n, dtype, dev):
+    if t is not None and (t.shape != (n,) or t.dtype != dtype or t.device != dev or not t.is_contiguous()):
+        raise ValueError(f"{fn}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, wanted ({n},) {dtype} on {dev}")
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(fn, ws, dev):
+    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"{fn}: the workspace is not a contiguous uint8 tensor on {dev}")
+
+
+class _On:
+    """The tensors' device as the current one, and the stream of the call on it; memory that
+    the call allocated is kept for a stream other than the current one."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream = dev, stream
+
+    def __enter__(self):
+        self.guard = None
+        if self.dev.index is not None and self.dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def handle(self, made):
+        if self.stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        for t in made:
+            if t is not None:
+                t.record_stream(self.stream)
+        return self.stream.cuda_stream
+
+
+def alloc_qk_norm_workspace(p, device="cuda") -> torch.Tensor:
+    n = int(lib().scope_qk_norm_workspace_bytes(ctypes.byref(p)))
+    if n == 0:
+        raise ScopeError("scope_qk_norm_workspace_bytes", 1)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def qk_norm_rope3d(p, Q, K, w_q=None, w_k=None, first=None, out_q=None, out_k=None, stream=None):
+    """RMS norm per head with a weight per channel, and 3D RoPE, of Q [B,H,N,d] and K
+    [B,Hkv,N,d] (K may be None) in one pass.  Strided tensors are taken as they are; out_q /
+    out_k may be Q / K.  first: int32 [B] positions of the entries' first tokens (default
+    p.first).  Returns (Yq, Yk)."""
+    fn, dev = "scope_qk_norm_rope3d", Q.device
+    with _On(dev, stream) as on:
+        Yq = torch.empty((p.B, p.H, p.N, p.d), dtype=Q.dtype, device=dev) if out_q is None else out_q
+        named = [("q", Q, (p.B, p.H, p.N, p.d)), ("yq", Yq, (p.B, p.H, p.N, p.d))]
+        Yk = out_k
+        if K is not None:
+            Yk = torch.empty((p.B, p.Hkv, p.N, p.d), dtype=K.dtype, device=dev) if out_k is None else out_k
+            named += [("k", K, (p.B, p.Hkv, p.N, p.d)), ("yk", Yk, (p.B, p.Hkv, p.N, p.d))]
+        lay = _tensors(fn, p, QkNormLayouts, named)
+        wq, wk = (_vector(fn, n, t, p.d, torch.float32, dev) for n, t in (("w_q", w_q), ("w_k", w_k)))
+        _check(fn, lib().scope_qk_norm_rope3d(
+            ctypes.byref(p), None if lay is None else ctypes.byref(lay), Q.data_ptr(),
+            None if K is None else K.data_ptr(), wq, wk, _vector(fn, "first", first, p.B, torch.int32, dev),
+            Yq.data_ptr(), None if Yk is None else Yk.data_ptr(), on.handle((Yq, Yk))))
+    return Yq, Yk
+
+
+def qk_norm_rope3d_backward(p, Q, K, w_q, w_k, dYq, dYk, first=None, ws=None, out_q=None, out_k=None, stream=None):
+    """Gradients of qk_norm_rope3d: (dQ, dK, dw_q, dw_k), dw float32 [d].  K and dYk may be
+    None (their gradients then are); out_q / out_k may be dYq / dYk."""
+    fn, dev = "scope_qk_norm_rope3d_backward", Q.device
+    with _On(dev, stream) as on:
+        ws = alloc_qk_norm_workspace(p, dev) if ws is None else ws
+        _workspace(fn, ws, dev)
+        dQ = torch.empty((p.B, p.H, p.N, p.d), dtype=Q.dtype, device=dev) if out_q is None else out_q
+        dw = torch.empty((2, p.d), dtype=torch.float32, device=dev)
+        dwq, dwk = dw[0], None
+        named = [(n, t, (p.B, p.H, p.N, p.d)) for n, t in (("q", Q), ("yq", dYq), ("dq", dQ))]
+        dK = out_k
+        if K is not None:
+            dK = torch.empty((p.B, p.Hkv, p.N, p.d), dtype=K.dtype, device=dev) if out_k is None else out_k
+            dwk = dw[1]
+            named += [(n, t, (p.B, p.Hkv, p.N, p.d)) for n, t in (("k", K), ("yk", dYk), ("dk", dK))]
+        lay = _tensors(fn, p, QkNormLayouts, named)
+        wq, wk = (_vector(fn, n, t, p.d, torch.float32, dev) for n, t in (("w_q", w_q), ("w_k", w_k)))
+        _check(fn, lib().scope_qk_norm_rope3d_backward(
+            ctypes.byref(p), None if lay is None else ctypes.byref(lay), Q.data_ptr(),
+            None if K is None else K.data_ptr(), wq, wk, dYq.data_ptr(), None if dYk is None else dYk.data_ptr(),
+            _vector(fn, "first", first, p.B, torch.int32, dev), dQ.data_ptr(), None if dK is None else dK.data_ptr(),
+            dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), ws.data_ptr(), ws.numel(),
+            on.handle((ws, dQ, dK, dw))))
+    return dQ, dK, dwq, dwk
+
+
+def alloc_window_workspace(p, device="cuda") -> torch.Tensor:
+    n = int(lib().scope_window_workspace_bytes(ctypes.byref(p)))
+    if n == 0:
+        raise ScopeError("scope_window_workspace_bytes", 1)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def window_attention(p, Q, K, V, q_first=None, k_len=None, ws=None, out=None, lse=False, stream=None):
+    """Attention of Q [B,H,Nq,d] over the keys K, V [B,Hkv,Nk,d] inside each query's window of
+    frames, and the first p.sinks frames.  q_first, k_len: int32 [B] position of each entry's
+    first query and its number of keys (default p.q_first and Nk).  Returns O, or (O, lse
+    [B,H,Nq] float32) with lse=True, which window_attention_backward needs."""
+    fn, dev = "scope_window_attention", Q.device
+    with _On(dev, stream) as on:
+        ws = alloc_window_workspace(p, dev) if ws is None else ws
+        _workspace(fn, ws, dev)
+        O = torch.empty((p.B, p.H, p.Nq, p.d), dtype=Q.dtype, device=dev) if out is None else out
+        L = torch.empty((p.B, p.H, p.Nq), dtype=torch.float32, device=dev) if lse else None
+        qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
+        lay = _tensors(fn, p, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", O, qs)))
+        _check(fn, lib().scope_window_attention(
+            ctypes.byref(p), None if lay is None else ctypes.byref(lay), Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+            _vector(fn, "q_first", q_first, p.B, torch.int32, dev), _vector(fn, "k_len", k_len, p.B, torch.int32, dev),
+            O.data_ptr(), None if L is None else L.data_ptr(), ws.data_ptr(), ws.numel(), on.handle((ws, O, L))))
+    return (O, L) if lse else O
+
+
+def window_attention_backward(p, Q, K, V, O, dO, lse, q_first=None, k_len=None, ws=None, out=None, stream=None):
+    """Gradients (dQ, dK, dV) of window_attention from its inputs, O and lse, and dO.  out: a
+    triple of tensors to write them to (strided ones too, e.g. the slices of one buffer)."""
+    fn, dev = "scope_window_attention_backward", Q.device
+    with _On(dev, stream) as on:
+        ws = alloc_window_workspace(p, dev) if ws is None else ws
+        _workspace(fn, ws, dev)
+        qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
+        if out is None:
+            dQ = torch.empty(qs, dtype=Q.dtype, device=dev)
+            dK, dV = torch.empty(ks, dtype=Q.dtype, device=dev), torch.empty(ks, dtype=Q.dtype, device=dev)
+        else:
+            dQ, dK, dV = out
+        if lse.shape != qs[:3] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+            raise ValueError(f"{fn}: lse is not a contiguous float32 tensor {qs[:3]} on {dev}")
+        lay = _tensors(fn, p, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", O, qs), ("d_o", dO, qs),
+                                              ("dq", dQ, qs), ("dk", dK, ks), ("dv", dV, ks)))
+        _check(fn, lib().scope_window_attention_backward(
+            ctypes.byref(p), None if lay is None else ctypes.byref(lay), Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+            O.data_ptr(), dO.data_ptr(), lse.data_ptr(), _vector(fn, "q_first", q_first, p.B, torch.int32, dev),
+            _vector(fn, "k_len", k_len, p.B, torch.int32, dev), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),
+            ws.data_ptr(), ws.numel(), on.handle((ws, dQ, dK, dV))))
+    return dQ, dK, dV
 
 
 def check_wait_timeout(p, wait_limit_ns, ws=None, stream=None):

@@ -1,0 +1,483 @@
+// Window attention with sinks on the CUDA cores: the fp32 form, forward and backward.
+//
+//   s_ij = q_i . k_j / sqrt d over the visible keys (window.cuh),  p = softmax(s),  O = p V
+//   with D_i = dO_i . O_i:  dV_j = sum_i p_ij dO_i,  ds_ij = p_ij (dO_i . v_j - D_i) / sqrt d,
+//   dQ_i = sum_j ds_ij k_j,  dK_j = sum_i ds_ij q_i.
+//
+// One block holds a tile of rows against tiles of 64 columns; both sides lie row-major in
+// shared memory with rows padded by 4 floats, so that the 16-byte reads of 16 neighbouring
+// rows meet different banks.  A thread owns rows ty + 16 i and columns tx + 16 j of a
+// score tile (4 x 4 scores from 8 16-byte reads per 4 channels, 64 FMAs), and rows ty + 16 i
+// and channels 4 tx + 64 j .. + 3 of an output.  Scores, softmax statistics and all sums are
+// fp32.  Bound by the FMA pipe (74 TFLOP/s).
+#include "window.cuh"
+
+namespace scope {
+
+namespace {
+
+constexpr int kBN = 64;      // columns of a score tile
+constexpr int kLdP = kBN + 4;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p);
+
+template <>
+__device__ __forceinline__ float4 load4<float>(const float *p)
+{
+    return *reinterpret_cast<const float4 *>(p);
+}
+
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p)
+{
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void store4(float *p, float4 v)
+{
+    *reinterpret_cast<float4 *>(p) = v;
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v)
+{
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// Rows of one tile to shared memory as fp32 (leading dimension D + 4); src(r) is row r's
+// address or NULL for a row of zeros.
+template <typename T, int D, int ROWS, int THREADS, typename Src>
+__device__ __forceinline__ void load_tile(float *dst, Src src)
+{
+    constexpr int C4 = D / 4;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < ROWS * C4; e += THREADS) {
+        const int r = e / C4, c = (e % C4) * 4;
+        const T *p = src(r);
+        store4(dst + r * (D + 4) + c, p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+}
+
+__device__ __forceinline__ void dot4(float &acc, float4 x, float4 y)
+{
+    acc = fmaf(x.x, y.x, acc);
+    acc = fmaf(x.y, y.y, acc);
+    acc = fmaf(x.z, y.z, acc);
+    acc = fmaf(x.w, y.w, acc);
+}
+
+// acc[i][j] = rows[ty + 16 i] . cols[tx + 16 j]
+template <int D, int MI>
+__device__ __forceinline__ void scores(float (&acc)[MI][4], const float *rows, const float *cols, int ty, int tx)
+{
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+        float4 x[MI], y[4];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) x[i] = *reinterpret_cast<const float4 *>(rows + (ty + 16 * i) * (D + 4) + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(cols + (tx + 16 * j) * (D + 4) + c);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dot4(acc[i][j], x[i], y[j]);
+    }
+}
+
+// out[i][4 jj + e] += sum_k w[ty + 16 i][k] cols[k][4 tx + 64 jj + e]
+template <int D, int MI>
+__device__ __forceinline__ void accumulate(float (&out)[MI][D / 16], const float *w, const float *cols, int ty, int tx)
+{
+#pragma unroll 2
+    for (int k = 0; k < kBN; k += 4) {
+        float4 p[MI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) p[i] = *reinterpret_cast<const float4 *>(w + (ty + 16 * i) * kLdP + k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+            for (int jj = 0; jj < D / 64; ++jj) {
+                const float4 v = *reinterpret_cast<const float4 *>(cols + (k + kk) * (D + 4) + 4 * tx + 64 * jj);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    const float pk = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                    out[i][4 * jj + 0] = fmaf(pk, v.x, out[i][4 * jj + 0]);
+                    out[i][4 * jj + 1] = fmaf(pk, v.y, out[i][4 * jj + 1]);
+                    out[i][4 * jj + 2] = fmaf(pk, v.z, out[i][4 * jj + 2]);
+                    out[i][4 * jj + 3] = fmaf(pk, v.w, out[i][4 * jj + 3]);
+                }
+            }
+        }
+    }
+}
+
+// Forward: BM rows of one unit (b, group of a.pack query heads) against one share of the key
+// tiles they see.  16 x 16 threads (BM = 64, 4 rows each) or 16 x 16 with one row each (BM =
+// 16, the form for few rows, which would leave most of a 64-row tile idle).
+template <typename T, int D, int BM>
+__global__ void __launch_bounds__(256) window_fwd_kernel(WinArgs a)
+{
+    constexpr int MI = BM / 16;
+    extern __shared__ __align__(16) float sm[];
+    float *sq = sm, *sk = sq + BM * (D + 4), *sv = sk + kBN * (D + 4), *sp = sv + kBN * (D + 4);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int rows = a.pack * a.Nq, tiles = (rows + BM - 1) / BM;
+    // item = ((unit * tiles) + tile) * splits + split
+    long long it = blockIdx.x;
+    const int split = (int)(it % a.splits);
+    it /= a.splits;
+    const int tile = (int)(it % tiles), unit = (int)(it / tiles);
+    const int groups = a.H / a.pack, b = unit / groups, h0 = (unit - b * groups) * a.pack;
+    const int hk = h0 / (a.H / a.Hkv);
+    const int r0 = tile * BM, r1 = min(rows, r0 + BM);
+    const int first = win_first(a, b), kl = win_klen(a, b);
+    // query range of the tile: rows r -> (head h0 + r / Nq, query r % Nq)
+    const bool wraps = r0 / a.Nq != (r1 - 1) / a.Nq;
+    const int ia = wraps ? 0 : r0 % a.Nq, iz = wraps ? a.Nq - 1 : (r1 - 1) % a.Nq;
+    const WinRow ra = win_row(a, first + ia, kl), rz = win_row(a, first + iz, kl);
+    const WinTiles wt = win_tiles<kBN>(ra, rz);
+    const int nt = wt.count(), t0 = (int)((long long)nt * split / a.splits), t1 = (int)((long long)nt * (split + 1) / a.splits);
+
+    load_tile<T, D, BM, 256>(sq, [&](int r) -> const T * {
+        const int rr = r0 + r;
+        return rr < r1 ? static_cast<const T *>(a.Q) + b * a.lq.b + (h0 + rr / a.Nq) * a.lq.h + (rr % a.Nq) * a.lq.n : nullptr;
+    });
+    WinRow lim[MI];
+    float m[MI], l[MI], o[MI][D / 16];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int rr = r0 + ty + 16 * i;
+        lim[i] = rr < r1 ? win_row(a, first + rr % a.Nq, kl) : WinRow{0, 0, 0};
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) o[i][e] = 0.f;
+    }
+    const T *kb = static_cast<const T *>(a.K) + b * a.lk.b + hk * a.lk.h;
+    const T *vb = static_cast<const T *>(a.V) + b * a.lv.b + hk * a.lv.h;
+    for (int t = t0; t < t1; ++t) {
+        const int j0 = wt.at(t) * kBN;
+        __syncthreads();
+        // keys and values that no row of the tile sees are not read (they may hold anything)
+        auto seen = [&](int j) { return j < ra.s || (j >= ra.lo && j < rz.hi); };
+        load_tile<T, D, kBN, 256>(sk, [&](int r) { return seen(j0 + r) ? kb + (j0 + r) * a.lk.n : nullptr; });
+        load_tile<T, D, kBN, 256>(sv, [&](int r) { return seen(j0 + r) ? vb + (j0 + r) * a.lv.n : nullptr; });
+        __syncthreads();
+        float s[MI][4];
+        scores<D, MI>(s, sq, sk, ty, tx);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            float mt = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = j0 + tx + 16 * j;
+                const bool vis = key < lim[i].s || (key >= lim[i].lo && key < lim[i].hi);
+                s[i][j] = vis ? s[i][j] * a.scale_log2 : -INFINITY;
+                mt = fmaxf(mt, s[i][j]);
+            }
+#pragma unroll
+            for (int x = 8; x; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+            const float mn = fmaxf(m[i], mt), base = mn == -INFINITY ? 0.f : mn;
+            const float corr = exp2f(m[i] - base);
+            float ls = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = exp2f(s[i][j] - base);
+                ls += s[i][j];
+                sp[(ty + 16 * i) * kLdP + tx + 16 * j] = s[i][j];
+            }
+#pragma unroll
+            for (int x = 8; x; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+            l[i] = l[i] * corr + ls;
+            m[i] = mn;
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) o[i][e] *= corr;
+        }
+        __syncwarp();   // a row of sp is written and read by one half warp
+        accumulate<D, MI>(o, sp, sv, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int rr = r0 + ty + 16 * i;
+        if (rr >= r1) continue;
+        const int h = h0 + rr / a.Nq, q = rr % a.Nq;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];   // no visible key: zeros; NaN stays NaN
+        const float lse2 = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
+        const long long row = win_row_index(a, b, h, q);
+        if (a.splits > 1) {
+            float *dst = a.part_o + (row * a.splits + split) * D;
+#pragma unroll
+            for (int jj = 0; jj < D / 64; ++jj)
+                store4(dst + 4 * tx + 64 * jj, make_float4(o[i][4 * jj] * inv, o[i][4 * jj + 1] * inv, o[i][4 * jj + 2] * inv,
+                                                           o[i][4 * jj + 3] * inv));
+            if (tx == 0) a.part_lse[row * a.splits + split] = lse2;
+        } else {
+            T *dst = static_cast<T *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n;
+#pragma unroll
+            for (int jj = 0; jj < D / 64; ++jj)
+                store4(dst + 4 * tx + 64 * jj, make_float4(o[i][4 * jj] * inv, o[i][4 * jj + 1] * inv, o[i][4 * jj + 2] * inv,
+                                                           o[i][4 * jj + 3] * inv));
+            if (tx == 0 && a.lse) a.lse[row] = lse2 * 0.6931471805599453f;
+        }
+    }
+}
+
+// Joins the key shares of every row: O = sum_s 2^(L_s - L) O_s with L = log2 sum_s 2^L_s.
+// One warp per row, shares in order (the result does not depend on the schedule).
+template <typename T, int D>
+__global__ void __launch_bounds__(128) window_join_kernel(WinArgs a)
+{
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= (long long)a.B * a.H * a.Nq) return;
+    const float *pl = a.part_lse + row * a.splits, *po = a.part_o + row * a.splits * D + lane * PER;
+    float m = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) m = (pl[s] > m || pl[s] != pl[s]) ? pl[s] : m;   // keeps a NaN
+    float sum = 0.f, o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    if (m != -INFINITY)
+        for (int s = 0; s < a.splits; ++s) {
+            const float w = exp2f(pl[s] - m);
+            sum += w;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[e] = fmaf(w, po[(long long)s * D + e], o[e]);
+        }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int i = (int)(row % a.Nq), h = (int)(row / a.Nq % a.H), b = (int)(row / a.Nq / a.H);
+    T *dst = static_cast<T *>(a.O) + b * a.lo.b + h * a.lo.h + i * a.lo.n + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        if constexpr (sizeof(T) == 2)
+            dst[e] = __float2bfloat16(o[e] * inv);
+        else
+            dst[e] = o[e] * inv;
+    }
+    if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+}
+
+// dQ: 64 query rows of one head against the key tiles they see; also writes D_i.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) window_dq_kernel(WinArgs a)
+{
+    constexpr int BM = 64, MI = 4;
+    extern __shared__ __align__(16) float sm[];
+    float *sq = sm, *sg = sq + BM * (D + 4), *sk = sg + BM * (D + 4), *sv = sk + kBN * (D + 4), *sp = sv + kBN * (D + 4);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tiles = (a.Nq + BM - 1) / BM;
+    const int tile = (int)(blockIdx.x % tiles), bh = (int)(blockIdx.x / tiles);
+    const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hkv);
+    const int r0 = tile * BM, r1 = min(a.Nq, r0 + BM);
+    const int first = win_first(a, b), kl = win_klen(a, b);
+    const WinRow ra = win_row(a, first + r0, kl), rz = win_row(a, first + r1 - 1, kl);
+    const WinTiles wt = win_tiles<kBN>(ra, rz);
+    const T *qb = static_cast<const T *>(a.Q) + b * a.lq.b + h * a.lq.h;
+    const T *gb = static_cast<const T *>(a.G) + b * a.lg.b + h * a.lg.h;
+    load_tile<T, D, BM, 256>(sq, [&](int r) { return r0 + r < r1 ? qb + (r0 + r) * a.lq.n : nullptr; });
+    load_tile<T, D, BM, 256>(sg, [&](int r) { return r0 + r < r1 ? gb + (r0 + r) * a.lg.n : nullptr; });
+    __syncthreads();
+    WinRow lim[MI];
+    float lse[MI], dl[MI], dq[MI][D / 16];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int q = r0 + ty + 16 * i;
+        const bool in = q < r1;
+        lim[i] = in ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
+        const long long row = win_row_index(a, b, h, in ? q : r0);
+        lse[i] = in ? a.lse[row] * 1.4426950408889634f : -INFINITY;
+        float s = 0.f;
+        if (in) {
+            const T *ob = static_cast<const T *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n;
+#pragma unroll
+            for (int jj = 0; jj < D / 64; ++jj) {
+                const int c = 4 * tx + 64 * jj;
+                dot4(s, load4<T>(ob + c), *reinterpret_cast<const float4 *>(sg + (ty + 16 * i) * (D + 4) + c));
+            }
+        }
+#pragma unroll
+        for (int x = 8; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        dl[i] = s;
+        if (in && tx == 0) a.delta[row] = s;
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) dq[i][e] = 0.f;
+    }
+    const T *kb = static_cast<const T *>(a.K) + b * a.lk.b + hk * a.lk.h;
+    const T *vb = static_cast<const T *>(a.V) + b * a.lv.b + hk * a.lv.h;
+    for (int t = 0; t < wt.count(); ++t) {
+        const int j0 = wt.at(t) * kBN;
+        __syncthreads();
+        auto seen = [&](int j) { return j < ra.s || (j >= ra.lo && j < rz.hi); };
+        load_tile<T, D, kBN, 256>(sk, [&](int r) { return seen(j0 + r) ? kb + (j0 + r) * a.lk.n : nullptr; });
+        load_tile<T, D, kBN, 256>(sv, [&](int r) { return seen(j0 + r) ? vb + (j0 + r) * a.lv.n : nullptr; });
+        __syncthreads();
+        float s[MI][4], dp[MI][4];
+        scores<D, MI>(s, sq, sk, ty, tx);
+        scores<D, MI>(dp, sg, sv, ty, tx);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = j0 + tx + 16 * j;
+                const bool vis = key < lim[i].s || (key >= lim[i].lo && key < lim[i].hi);
+                sp[(ty + 16 * i) * kLdP + tx + 16 * j] =
+                    vis ? exp2f(fmaf(s[i][j], a.scale_log2, -lse[i])) * (dp[i][j] - dl[i]) : 0.f;
+            }
+        __syncwarp();
+        accumulate<D, MI>(dq, sp, sk, ty, tx);
+    }
+    T *dst = static_cast<T *>(a.dQ) + b * a.ldq.b + h * a.ldq.h;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int q = r0 + ty + 16 * i;
+        if (q >= r1) continue;
+#pragma unroll
+        for (int jj = 0; jj < D / 64; ++jj)
+            store4(dst + q * a.ldq.n + 4 * tx + 64 * jj,
+                   make_float4(dq[i][4 * jj] * a.scale, dq[i][4 * jj + 1] * a.scale, dq[i][4 * jj + 2] * a.scale,
+                               dq[i][4 * jj + 3] * a.scale));
+    }
+}
+
+// dK, dV: 64 keys of one key head against every query (of all its query heads, in order) that
+// may see one of them.  Scores are taken transposed: rows are keys, columns are queries.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) window_dkv_kernel(WinArgs a)
+{
+    constexpr int BM = 64, MI = 4;
+    extern __shared__ __align__(16) float sm[];
+    float *sk = sm, *sv = sk + BM * (D + 4), *sq = sv + BM * (D + 4), *sg = sq + kBN * (D + 4), *sp = sg + kBN * (D + 4),
+          *sd = sp + BM * kLdP;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    // sink blocks meet every later query: they come first in launch order
+    const int units = a.B * a.Hkv;
+    const int tile = (int)(blockIdx.x / units), bh = (int)(blockIdx.x % units);
+    const int b = bh / a.Hkv, hk = bh - b * a.Hkv, G = a.H / a.Hkv;
+    const int j0 = tile * BM, j1 = min(a.Nk, j0 + BM);
+    const int first = win_first(a, b), kl = win_klen(a, b);
+    const int2 qr = win_queries(a, first, kl, a.Nq, j0, j1);
+    const T *kb = static_cast<const T *>(a.K) + b * a.lk.b + hk * a.lk.h;
+    const T *vb = static_cast<const T *>(a.V) + b * a.lv.b + hk * a.lv.h;
+    load_tile<T, D, BM, 256>(sk, [&](int r) { return j0 + r < min(j1, kl) ? kb + (j0 + r) * a.lk.n : nullptr; });
+    load_tile<T, D, BM, 256>(sv, [&](int r) { return j0 + r < min(j1, kl) ? vb + (j0 + r) * a.lv.n : nullptr; });
+    float dk[MI][D / 16], dv[MI][D / 16];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) dk[i][e] = dv[i][e] = 0.f;
+    for (int g = 0; g < G; ++g) {
+        const int h = hk * G + g;
+        const T *qb = static_cast<const T *>(a.Q) + b * a.lq.b + h * a.lq.h;
+        const T *gb = static_cast<const T *>(a.G) + b * a.lg.b + h * a.lg.h;
+        for (int i0 = qr.x; i0 < qr.y; i0 += kBN) {
+            __syncthreads();
+            load_tile<T, D, kBN, 256>(sq, [&](int r) { return i0 + r < qr.y ? qb + (i0 + r) * a.lq.n : nullptr; });
+            load_tile<T, D, kBN, 256>(sg, [&](int r) { return i0 + r < qr.y ? gb + (i0 + r) * a.lg.n : nullptr; });
+            __syncthreads();
+            float s[MI][4], dp[MI][4];
+            scores<D, MI>(s, sk, sq, ty, tx);
+            scores<D, MI>(dp, sv, sg, ty, tx);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int q = i0 + tx + 16 * j;
+                const bool in = q < qr.y;
+                const WinRow lim = in ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
+                const long long row = win_row_index(a, b, h, in ? q : 0);
+                const float lse = a.lse[row] * 1.4426950408889634f, dl = a.delta[row];
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    const int key = j0 + ty + 16 * i;
+                    const bool vis = key < lim.s || (key >= lim.lo && key < lim.hi);
+                    const float p = vis ? exp2f(fmaf(s[i][j], a.scale_log2, -lse)) : 0.f;
+                    sp[(ty + 16 * i) * kLdP + tx + 16 * j] = p;
+                    sd[(ty + 16 * i) * kLdP + tx + 16 * j] = vis ? p * (dp[i][j] - dl) : 0.f;
+                }
+            }
+            __syncwarp();
+            accumulate<D, MI>(dv, sp, sg, ty, tx);
+            accumulate<D, MI>(dk, sd, sq, ty, tx);
+        }
+    }
+    T *dkb = static_cast<T *>(a.dK) + b * a.ldk.b + hk * a.ldk.h, *dvb = static_cast<T *>(a.dV) + b * a.ldv.b + hk * a.ldv.h;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int j = j0 + ty + 16 * i;
+        if (j >= j1) continue;
+#pragma unroll
+        for (int jj = 0; jj < D / 64; ++jj) {
+            const int c = 4 * tx + 64 * jj;
+            store4(dkb + j * a.ldk.n + c, make_float4(dk[i][4 * jj] * a.scale, dk[i][4 * jj + 1] * a.scale,
+                                                      dk[i][4 * jj + 2] * a.scale, dk[i][4 * jj + 3] * a.scale));
+            store4(dvb + j * a.ldv.n + c, make_float4(dv[i][4 * jj], dv[i][4 * jj + 1], dv[i][4 * jj + 2], dv[i][4 * jj + 3]));
+        }
+    }
+}
+
+template <typename F>
+cudaError_t launch(F *kernel, long long grid, int smem, const WinArgs &a, cudaStream_t s)
+{
+    if (grid < 1 || grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)grid, 256, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t forward(const WinArgs &a, cudaStream_t s)
+{
+    // 16-row tiles when a unit's rows fill at most one of them, 64-row tiles otherwise
+    const long long rows = (long long)a.pack * a.Nq, units = (long long)a.B * (a.H / a.pack);
+    if (rows <= 16)
+        return launch(window_fwd_kernel<T, D, 16>, units * a.splits, (16 + 2 * kBN) * (D + 4) * 4 + 16 * kLdP * 4, a, s);
+    return launch(window_fwd_kernel<T, D, 64>, units * ((rows + 63) / 64) * a.splits,
+                  (64 + 2 * kBN) * (D + 4) * 4 + 64 * kLdP * 4, a, s);
+}
+
+template <typename T, int D>
+cudaError_t backward(const WinArgs &a, cudaStream_t s)
+{
+    cudaError_t e = launch(window_dq_kernel<T, D>, (long long)a.B * a.H * ((a.Nq + 63) / 64),
+                           4 * 64 * (D + 4) * 4 + 64 * kLdP * 4, a, s);
+    if (e != cudaSuccess) return e;
+    return launch(window_dkv_kernel<T, D>, (long long)a.B * a.Hkv * ((a.Nk + 63) / 64),
+                  4 * 64 * (D + 4) * 4 + 2 * 64 * kLdP * 4, a, s);
+}
+
+}  // namespace
+
+cudaError_t window_simt_forward(const WinArgs &a, cudaStream_t s)
+{
+    if (a.is_bf16) return a.d == 64 ? forward<__nv_bfloat16, 64>(a, s) : forward<__nv_bfloat16, 128>(a, s);
+    return a.d == 64 ? forward<float, 64>(a, s) : forward<float, 128>(a, s);
+}
+
+cudaError_t window_simt_backward(const WinArgs &a, cudaStream_t s)
+{
+    if (a.is_bf16) return a.d == 64 ? backward<__nv_bfloat16, 64>(a, s) : backward<__nv_bfloat16, 128>(a, s);
+    return a.d == 64 ? backward<float, 64>(a, s) : backward<float, 128>(a, s);
+}
+
+cudaError_t window_join(const WinArgs &a, cudaStream_t s)
+{
+    const long long rows = (long long)a.B * a.H * a.Nq;
+    const unsigned grid = (unsigned)((rows + 3) / 4);
+    if (a.is_bf16) {
+        if (a.d == 64) window_join_kernel<__nv_bfloat16, 64><<<grid, 128, 0, s>>>(a);
+        else window_join_kernel<__nv_bfloat16, 128><<<grid, 128, 0, s>>>(a);
+    } else {
+        if (a.d == 64) window_join_kernel<float, 64><<<grid, 128, 0, s>>>(a);
+        else window_join_kernel<float, 128><<<grid, 128, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace scope

@@ -399,6 +399,126 @@ scope_status scope_check_wait_timeout(const scope_params *p, uint64_t wait_limit
  */
 scope_status scope_tc_accumulation_probe(const void *A, const void *B, int K, int N, float *D, void *stream);
 
+/*
+ * Norm of queries and keys with 3D RoPE, and attention over a sliding window with sinks
+ * ------------------------------------------------------------------------------------
+ * Two steps a video diffusion transformer's attention layer has beside the ones above, each
+ * with its gradients (the SCOPE paper has no counterpart).  They take tensors [B, heads, N, d]
+ * with strides, grouped key heads, and a run of tokens that need not start at position 0 (the
+ * newest frames or the newest token over a cache).  The conventions at the top hold, except:
+ *  - Strides: channels are contiguous; a scope_strides gives the distances of batch entries,
+ *    heads and tokens in elements (all zero: dense [B, heads, N, d]).  A stride of a dimension
+ *    longer than one is a positive multiple of 16 bytes, and no two elements share a place
+ *    (else SCOPE_ERR_INVALID_ARGUMENT); elements between the rows are neither read nor written.
+ *    A layouts pointer of NULL means that every tensor is dense.
+ *  - Limits: d in {64, 128}; N, Nq, Nk <= 2^24; B * heads <= 2^20; B * heads * tokens < 2^31;
+ *    positions of first tokens <= 2^30 (else SCOPE_ERR_UNSUPPORTED).
+ *  - Outputs must not overlap inputs, except where stated.  Sums are taken in a fixed order:
+ *    the same call gives the same bits.
+ */
+typedef struct {
+    int64_t batch, head, token;
+} scope_strides;
+
+/* Shape of one query/key norm.  Token i of batch entry b stands at position first + i (first:
+ * the device array's entry b where that is given): frame t = position / (Hg*Wg), row h and
+ * column w inside it.  d_t, d_h, d_w: even channel ranges that sum to d; a range may be empty
+ * (d_t = d: one-dimensional RoPE by t).  Keys have Hkv heads, queries H. */
+typedef struct {
+    int B, H, Hkv, N;
+    int d, d_t, d_h, d_w;
+    int Hg, Wg;
+    int first;           /* 0 .. 2^30 */
+    double eps;          /* 0 .. 1 */
+    double base;         /* > 0 */
+    scope_dtype dtype;
+} scope_qk_norm_params;
+
+/* Layouts: q, k inputs; yq, yk outputs (backward: their gradients); dq, dk gradients. */
+typedef struct {
+    scope_strides q, k, yq, yk, dq, dk;
+} scope_qk_norm_layouts;
+
+/* Workspace bytes of scope_qk_norm_rope3d_backward (0 if p is invalid); forward needs none. */
+size_t scope_qk_norm_workspace_bytes(const scope_qk_norm_params *p);
+
+/*
+ * y = R(w o x / sqrt(mean_c x_c^2 + eps)) for every row x of Q and of K, R the rotation of
+ * scope_rope3d at the row's position.
+ *   Q [B,H,N,d], K [B,Hkv,N,d] dtype (K and Yk may both be NULL); Yq, Yk out, same shapes; an
+ *   output may be its own input (same address and layout)
+ *   w_q, w_k  [d] float, or NULL for ones
+ *   first     [B] int32 device positions of the entries' first tokens, or NULL for p->first
+ *             (values outside [0, 2^30] are clamped)
+ * Angles are binary64 (reduced to a turn before cos and sin in fp32), sums and products fp32,
+ * one rounding to dtype.  No workspace; allocates nothing; one launch.
+ */
+scope_status scope_qk_norm_rope3d(const scope_qk_norm_params *p, const scope_qk_norm_layouts *lay, const void *Q,
+                                  const void *K, const float *w_q, const float *w_k, const int32_t *first, void *Yq,
+                                  void *Yk, void *stream);
+
+/*
+ * Gradients of scope_qk_norm_rope3d from dYq, dYk (laid out by yq, yk) and the forward's
+ * inputs: dQ, dK (dtype, laid out by dq, dk; may be dYq, dYk in place with the same layout) and
+ * the weights' dw_q, dw_k [d] float (either may be NULL), summed over all rows in fp32.
+ *   ws  at least scope_qk_norm_workspace_bytes(p) bytes
+ */
+scope_status scope_qk_norm_rope3d_backward(const scope_qk_norm_params *p, const scope_qk_norm_layouts *lay,
+                                           const void *Q, const void *K, const float *w_q, const float *w_k,
+                                           const void *dYq, const void *dYk, const int32_t *first, void *dQ, void *dK,
+                                           float *dw_q, float *dw_k, void *ws, size_t ws_bytes, void *stream);
+
+/* Shape and window of one windowed attention.  Positions fall into frames of `frame` tokens
+ * (1: a window of tokens), f(x) = x / frame.  Query i of batch entry b stands at position
+ * p = q_first + i; it sees key j iff
+ *   j < k_len,  f(j) <= f(p) + right,  and  f(j) >= f(p) - left  or  f(j) < sinks
+ * (left, right: -1 = unbounded; right = 0: causal by frame).  Query heads share key heads in
+ * groups: head h reads key head h / (H / Hkv). */
+typedef struct {
+    int B, H, Hkv;       /* H a multiple of Hkv */
+    int Nq, Nk, d;
+    int frame;           /* 1 .. 2^24 */
+    int left, right;     /* frames, -1 .. 2^30 */
+    int sinks;           /* frames, 0 .. 2^30 */
+    int q_first;         /* 0 .. 2^30 */
+    scope_dtype dtype;
+} scope_window_params;
+
+typedef struct {
+    scope_strides q, k, v, o, d_o, dq, dk, dv;
+} scope_window_layouts;
+
+/* Workspace bytes of both calls below (0 if p is invalid). */
+size_t scope_window_workspace_bytes(const scope_window_params *p);
+
+/*
+ * O_i = sum_j softmax_j(q_i . k_j / sqrt d) v_j over the visible keys; zeros for a query that
+ * sees none.
+ *   Q [B,H,Nq,d], K, V [B,Hkv,Nk,d] dtype; O out [B,H,Nq,d]
+ *   q_first  [B] int32 (device) positions of the entries' first queries, or NULL for
+ *            p->q_first (values outside [0, 2^30] are clamped)
+ *   k_len    [B] int32 (device) keys of each entry, or NULL for Nk (clamped to [0, Nk])
+ *   lse      out [B,H,Nq] float log sum exp of each row's scaled logits (-inf: no key), or NULL
+ * Keys and values at or beyond k_len may hold anything.  Keys that a query does not see do not
+ * touch its output; a value row that is not finite can reach the outputs of other queries
+ * of the same 256 that do see a neighbouring key.
+ */
+scope_status scope_window_attention(const scope_window_params *p, const scope_window_layouts *lay, const void *Q,
+                                    const void *K, const void *V, const int32_t *q_first, const int32_t *k_len, void *O,
+                                    float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients from dO and the forward's inputs, O and lse:  with P = exp(s - lse) and
+ * D_i = dO_i . O_i,  dV = P^T dO,  dS = P o (dO V^T - D),  dQ = dS K / sqrt d,
+ * dK = dS^T Q / sqrt d; dK and dV summed over the query heads of their group.  Every row is
+ * written: zeros for queries that see no key and keys that no query sees.
+ *   dO [B,H,Nq,d] dtype; dQ like Q, dK, dV like K, V (dtype)
+ */
+scope_status scope_window_attention_backward(const scope_window_params *p, const scope_window_layouts *lay,
+                                             const void *Q, const void *K, const void *V, const void *O, const void *dO,
+                                             const float *lse, const int32_t *q_first, const int32_t *k_len, void *dQ,
+                                             void *dK, void *dV, void *ws, size_t ws_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *scope_status_string(scope_status s);
 

@@ -1,0 +1,400 @@
+"""Window attention with sinks and the query/key norm with RoPE on the GPU, forward and
+backward, against the binary64 forms and bounds of window_common."""
+import math
+
+import pytest
+import torch
+
+from free_sparse_attention_b200 import capi
+from window_common import angles, attention, check, norm, visible
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": (torch.bfloat16, capi.SCOPE_BF16), "f32": (torch.float32, capi.SCOPE_F32)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from free_sparse_attention_b200.build import build
+    build()
+    capi.lib()
+
+
+def _randn(shape, dtype, seed, gain=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * gain).to(dtype).cuda()
+
+
+def _params(dtype, B=1, H=2, Hkv=None, Nq=100, Nk=None, d=64, frame=1, left=20, right=0, sinks=0, q_first=0):
+    return capi.WindowParams(B=B, H=H, Hkv=Hkv or H, Nq=Nq, Nk=Nk or Nq, d=d, frame=frame, left=left, right=right,
+                             sinks=sinks, q_first=q_first, dtype=DT[dtype][1])
+
+
+def _inputs(p, dtype, seed=0):
+    dt = DT[dtype][0]
+    return (_randn((p.B, p.H, p.Nq, p.d), dt, seed, 1.5), _randn((p.B, p.Hkv, p.Nk, p.d), dt, seed + 1),
+            _randn((p.B, p.Hkv, p.Nk, p.d), dt, seed + 2), _randn((p.B, p.H, p.Nq, p.d), dt, seed + 3))
+
+
+def _run(p, dtype, q_first=None, k_len=None, seed=0, backward=True):
+    Q, K, V, G = _inputs(p, dtype, seed)
+    dev = lambda v: None if v is None else torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    at = {"q_first": dev(q_first), "k_len": dev(k_len)}
+    vis = visible(p, q_first or [p.q_first] * p.B, k_len or [p.Nk] * p.B)
+    ref = attention(Q, K, V, vis, G if backward else None)
+    ws = capi.alloc_window_workspace(p)
+    O, lse = capi.window_attention(p, Q, K, V, ws=ws, lse=True, **at)
+    torch.cuda.synchronize()
+    assert capi.get_device_status(ws) == 0
+    check("O", O, *ref["O"])
+    check("lse", lse, *ref["lse"])
+    if backward:
+        dQ, dK, dV = capi.window_attention_backward(p, Q, K, V, O, G, lse, ws=ws, **at)
+        torch.cuda.synchronize()
+        assert capi.get_device_status(ws) == 0
+        for n, t in (("dQ", dQ), ("dK", dK), ("dV", dV)):
+            check(n, t, *ref[n])
+    return O
+
+
+SHAPES = [
+    dict(Nq=1), dict(Nq=2, left=0), dict(Nq=63), dict(Nq=64, right=3), dict(Nq=65, d=128, sinks=2),
+    dict(Nq=127, left=200), dict(Nq=129, d=128, left=7, right=5), dict(Nq=257, H=1, left=40, sinks=5),
+    dict(Nq=300, left=-1, right=0, d=128), dict(Nq=300, left=-1, right=-1),
+    dict(Nq=390, frame=130, left=1, right=1, sinks=1), dict(Nq=513, frame=7, left=4, right=2, sinks=3, d=128),
+    dict(Nq=400, left=3, sinks=400), dict(Nq=260, frame=1000, left=0, right=0), dict(Nq=700, left=-1, right=2, sinks=9),
+    dict(B=2, H=6, Hkv=2, Nq=333, left=50, sinks=4, d=128), dict(B=1, H=8, Hkv=1, Nq=150, left=33, right=0),
+    dict(Nq=100, Nk=500, left=90, q_first=400, sinks=2), dict(Nq=130, Nk=900, frame=64, left=3, q_first=770, d=128),
+    dict(Nq=5, Nk=1000, left=600, q_first=995, sinks=1, H=4, Hkv=2), dict(Nq=200, Nk=90, left=30),
+    dict(Nq=70, Nk=64, left=5, q_first=40),          # the last queries' windows lie past the keys
+    dict(Nq=64, Nk=64, left=5, q_first=1 << 30),     # every window does
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()))
+def test_window_attention_and_gradients(shape, dtype):
+    _run(_params(dtype, **shape), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape,q_first,k_len", [
+    (dict(B=3, Nq=200, left=30, sinks=2), None, [200, 77, 0]),
+    (dict(B=3, Nq=200, left=30), None, [1, 130, 64]),
+    (dict(B=4, H=8, Hkv=2, Nq=1, Nk=700, left=255, sinks=4, d=128), [699, 0, 511, 63], [700, 1, 512, 64]),
+    (dict(B=2, H=4, Hkv=4, Nq=90, Nk=700, frame=30, left=2, right=0, sinks=1), [600, 210], [690, 300]),
+    (dict(B=2, Nq=64, Nk=128, left=10, right=10), [1 << 20, -5], [1000, -3]),     # clamped
+])
+def test_window_attention_lengths_and_positions_per_entry(shape, q_first, k_len, dtype):
+    p = _params(dtype, **shape)
+    B = p.B
+    # the reference takes the clamped values
+    if q_first and min(q_first) < 0:
+        Q, K, V, _ = _inputs(p, dtype)
+        O = capi.window_attention(p, Q, K, V, q_first=torch.tensor(q_first, dtype=torch.int32, device="cuda"),
+                                  k_len=torch.tensor(k_len, dtype=torch.int32, device="cuda"))
+        vis = visible(p, [max(x, 0) for x in q_first], [min(max(n, 0), p.Nk) for n in k_len])
+        check("O", O, *attention(Q, K, V, vis)["O"])
+    else:
+        _run(p, dtype, q_first or [0] * B, k_len)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Nq,H,Hkv", [(1, 1, 1), (1, 5, 5), (1, 32, 4), (1, 40, 1), (3, 8, 2), (16, 1, 1), (17, 2, 1), (40, 2, 2)])
+def test_few_rows_over_a_long_cache(Nq, H, Hkv, dtype):
+    """The split form: shares of a long key range joined, with sinks and without a window."""
+    n = 9001
+    for left, sinks, d in ((4095, 4, 128), (-1, 0, 64), (60, 70, 128)):
+        p = _params(dtype, H=H, Hkv=Hkv, Nq=Nq, Nk=n, d=d, left=left, right=0, sinks=sinks, q_first=n - Nq)
+        _run(p, dtype, backward=Nq == 3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strided_tensors(dtype):
+    """Slices of one [B, N, 3, H, d] buffer in, slices of another out, forward and backward."""
+    p = _params(dtype, B=2, H=3, Nq=150, d=64, left=40, right=4, sinks=3)
+    dt = DT[dtype][0]
+    qkv = _randn((p.B, p.Nq, 3, p.H, p.d), dt, 5)
+    Q, K, V = (qkv[:, :, i].transpose(1, 2) for i in range(3))
+    out = torch.zeros((p.B, p.Nq, p.H, p.d + 64), dtype=dt, device="cuda")
+    O = out[..., :p.d].transpose(1, 2)
+    _, lse = capi.window_attention(p, Q, K, V, out=O, lse=True)
+    G = _randn((p.B, p.Nq, p.H, p.d), dt, 6).transpose(1, 2)
+    ref = attention(Q, K, V, visible(p, [0] * p.B, [p.Nk] * p.B), G)
+    check("O", O, *ref["O"])
+    assert (out[..., p.d:] == 0).all()
+    grad = torch.zeros_like(qkv)
+    outs = tuple(grad[:, :, i].transpose(1, 2) for i in range(3))
+    capi.window_attention_backward(p, Q, K, V, O, G, lse, out=outs)
+    for n, t in zip(("dQ", "dK", "dV"), outs):
+        check(n, t, *ref[n])
+    # the same values as from dense copies
+    dense = capi.window_attention(p, Q.contiguous(), K.contiguous(), V.contiguous())
+    assert torch.equal(dense, O)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Nq", [300, 1])
+def test_what_lies_behind_the_keys_is_not_used(dtype, Nq):
+    """NaN and infinity at and beyond k_len, in the keys and in the values."""
+    p = _params(dtype, B=2, H=2, Nq=Nq, Nk=300, d=128, left=70, right=70, sinks=2)
+    Q, K, V, G = _inputs(p, dtype, 9)
+    k_len = [171, 40]
+    first = torch.tensor([max(n - Nq, 0) if Nq == 1 else 0 for n in k_len], dtype=torch.int32, device="cuda")
+    lens = torch.tensor(k_len, dtype=torch.int32, device="cuda")
+    O, lse = capi.window_attention(p, Q, K, V, q_first=first, k_len=lens, lse=True)
+    grads = capi.window_attention_backward(p, Q, K, V, O, G, lse, q_first=first, k_len=lens)
+    Kn, Vn = K.clone(), V.clone()
+    for b, n in enumerate(k_len):
+        Kn[b, :, n:] = float("nan")
+        Vn[b, :, n:] = float("inf")
+        Vn[b, :, n + 1:] = float("nan")
+    O2, lse2 = capi.window_attention(p, Q, Kn, Vn, q_first=first, k_len=lens, lse=True)
+    again = capi.window_attention_backward(p, Q, Kn, Vn, O2, G, lse2, q_first=first, k_len=lens)
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    for x, y in zip(grads, again):
+        assert torch.equal(x, y)
+    for b, n in enumerate(k_len):
+        assert (again[1][b, :, n:] == 0).all() and (again[2][b, :, n:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Nq", [200, 1])
+def test_hidden_keys_that_are_not_finite_change_nothing_and_visible_ones_show(dtype, Nq):
+    p = _params(dtype, Nq=Nq, Nk=200, d=64, left=20, right=0, q_first=200 - Nq)
+    Q, K, V, _ = _inputs(p, dtype, 11)
+    O = capi.window_attention(p, Q, K, V)
+    Kn = K.clone()
+    Kn[:, :, 30] = float("nan")
+    On = capi.window_attention(p, Q, Kn, V)
+    sees = visible(p, [p.q_first], [p.Nk])[0][:, 30]
+    assert torch.equal(On[:, :, ~sees], O[:, :, ~sees])
+    assert torch.isnan(On[:, :, sees]).all()
+    if Nq == 1:
+        Kn = K.clone()
+        Kn[:, :, 190] = float("nan")
+        assert torch.isnan(capi.window_attention(p, Q, Kn, V)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_logits(dtype):
+    """Logits of hundreds, growing along the keys: the running maximum rescales every tile."""
+    p = _params(dtype, Nq=140, Nk=600, d=64, left=-1, right=-1)
+    Q, K, V, G = _inputs(p, dtype, 13)
+    K = K + (torch.arange(600, device="cuda") / 25.0)[:, None].to(K.dtype) * Q[:, :, :1].sign()
+    Q = Q.abs() * Q[:, :, :1].sign()
+    ref = attention(Q, K, V, visible(p, [0], [600]), None)
+    O = capi.window_attention(p, Q, K, V)
+    check("O", O, *ref["O"])
+
+
+def test_gradients_against_differences():
+    """Central differences of the binary64 forward along random directions."""
+    p = _params("f32", B=1, H=4, Hkv=2, Nq=96, d=64, left=30, right=2, sinks=2)
+    Q, K, V, G = _inputs(p, "f32", 17)
+    vis = visible(p, [0], [p.Nk])
+    O, lse = capi.window_attention(p, Q, K, V, lse=True)
+    grads = capi.window_attention_backward(p, Q, K, V, O, G, lse)
+    loss = lambda *x: (attention(*x, vis)["O"][0] * G.double()).sum().item()  # noqa: E731
+    xs = [Q.double(), K.double(), V.double()]
+    h = 1e-5
+    for i, g in enumerate(grads):
+        for seed in range(3):
+            e = _randn(xs[i].shape, torch.float32, 100 + seed).double()
+            up, dn = list(xs), list(xs)
+            up[i], dn[i] = xs[i] + h * e, xs[i] - h * e
+            num = (loss(*up) - loss(*dn)) / (2 * h)
+            got = (g.double() * e).sum().item()
+            # difference error ~ h^2 third derivative and 1e-16 |L| / h; kernel error ~ 1e-6 per term
+            assert abs(num - got) <= 1e-4 * (g.double().abs() * e.abs()).sum().item()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_same_bits_again_and_rows_do_not_mix(dtype):
+    p = _params(dtype, B=2, H=4, Hkv=2, Nq=500, d=128, left=100, right=10, sinks=4)
+    Q, K, V, G = _inputs(p, dtype, 19)
+    O, lse = capi.window_attention(p, Q, K, V, lse=True)
+    grads = capi.window_attention_backward(p, Q, K, V, O, G, lse)
+    for _ in range(3):
+        O2, lse2 = capi.window_attention(p, Q, K, V, lse=True)
+        assert torch.equal(O, O2) and torch.equal(lse, lse2)
+        for x, y in zip(grads, capi.window_attention_backward(p, Q, K, V, O2, G, lse2)):
+            assert torch.equal(x, y)
+    # batch entry 1 alone gives its own rows
+    p1 = _params(dtype, B=1, H=4, Hkv=2, Nq=500, d=128, left=100, right=10, sinks=4)
+    assert torch.equal(capi.window_attention(p1, Q[1:], K[1:], V[1:])[0], O[1])
+
+
+@pytest.mark.parametrize("Nq", [1, 300])
+def test_captured_and_replayed_on_another_stream(Nq):
+    """Forward and backward in one graph, replayed with new inputs in the same buffers."""
+    p = _params("bf16", H=4, Nq=Nq, Nk=1300, d=128, left=999, q_first=1300 - Nq, sinks=4)
+    Q, K, V, G = _inputs(p, "bf16", 23)
+    ws = capi.alloc_window_workspace(p)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        O, lse = capi.window_attention(p, Q, K, V, ws=ws, lse=True)
+        capi.window_attention_backward(p, Q, K, V, O, G, lse, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        O, lse = capi.window_attention(p, Q, K, V, ws=ws, lse=True)
+        dQ, dK, dV = capi.window_attention_backward(p, Q, K, V, O, G, lse, ws=ws)
+    for seed in (30, 40):
+        for t, x in zip((Q, K, V, G), _inputs(p, "bf16", seed)):
+            t.copy_(x)
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.default_stream())
+            graph.replay()
+        torch.cuda.synchronize()
+        O2, lse2 = capi.window_attention(p, Q, K, V, lse=True, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(O, O2)
+        for x, y in zip((dQ, dK, dV), capi.window_attention_backward(p, Q, K, V, O2, G, lse2)):
+            assert torch.equal(x, y)
+
+
+def test_whole_layer_sampled_rows():
+    """17550 tokens in frames of 1350, 6 of 48 heads: rows of the first, a middle and the last
+    frame against the binary64 form of those rows."""
+    p = _params("bf16", H=6, Nq=17550, d=64, frame=1350, left=1, right=1, sinks=1)
+    Q, K, V, _ = _inputs(p, "bf16", 29)
+    O = capi.window_attention(p, Q, K, V)
+    for r0 in (0, 1349, 8000, 17500):
+        r1 = min(r0 + 50, 17550)
+        pr = _params("bf16", H=6, Nq=r1 - r0, Nk=17550, d=64, frame=1350, left=1, right=1, sinks=1, q_first=r0)
+        ref = attention(Q[:, :, r0:r1], K, V, visible(pr, [r0], [17550]))
+        check("O", O[:, :, r0:r1], *ref["O"])
+
+
+# ------------------------------------------------------------------------------ norm + RoPE
+def _norm_params(dtype, B=1, H=2, Hkv=None, N=50, split=(16, 24, 24), Hg=5, Wg=7, first=0, eps=1e-6, base=10000.0):
+    return capi.QkNormParams(B=B, H=H, Hkv=Hkv or H, N=N, d=sum(split), d_t=split[0], d_h=split[1], d_w=split[2],
+                             Hg=Hg, Wg=Wg, first=first, eps=eps, base=base, dtype=DT[dtype][1])
+
+
+NORMS = [
+    dict(N=1), dict(N=1, H=24, first=123456, Hg=45, Wg=80, split=(16, 56, 56)), dict(N=31), dict(N=33, H=5, Hkv=1),
+    dict(B=3, N=257, H=7, Hkv=3, split=(44, 42, 42)), dict(N=1000, H=1, split=(128, 0, 0), Hg=1, Wg=1, first=1 << 20),
+    dict(N=77, split=(0, 64, 0), Hg=40, Wg=1), dict(N=64, split=(0, 0, 128), Hg=1, Wg=1000, base=500.0),
+    dict(N=130, split=(22, 20, 22), eps=0.0), dict(N=2000, H=48, Hkv=48, Hg=30, Wg=45),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", NORMS, ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()).replace(" ", ""))
+def test_qk_norm_rope3d_and_gradients(shape, dtype):
+    p = _norm_params(dtype, **shape)
+    dt = DT[dtype][0]
+    first = [p.first + 13 * b for b in range(p.B)]
+    cs, sn = angles(p, first)
+    at = torch.tensor(first, dtype=torch.int32, device="cuda") if p.B > 1 else None
+    Q, K = _randn((p.B, p.H, p.N, p.d), dt, 1, 1.7), _randn((p.B, p.Hkv, p.N, p.d), dt, 2, 0.3)
+    Gq, Gk = _randn(Q.shape, dt, 3), _randn(K.shape, dt, 4)
+    wq, wk = 1 + 0.3 * _randn((p.d,), torch.float32, 5), 1 + 0.3 * _randn((p.d,), torch.float32, 6)
+    Yq, Yk = capi.qk_norm_rope3d(p, Q, K, wq, wk, first=at)
+    dQ, dK, dwq, dwk = capi.qk_norm_rope3d_backward(p, Q, K, wq, wk, Gq, Gk, first=at)
+    torch.cuda.synchronize()
+    for X, w, G, Y, dX, dw in ((Q, wq, Gq, Yq, dQ, dwq), (K, wk, Gk, Yk, dK, dwk)):
+        ref = norm(X, w, cs, sn, p.eps, G)
+        check("Y", Y, *ref["Y"])
+        check("dX", dX, *ref["dX"])
+        check("dw", dw, *ref["dw"])
+    # queries only, no weights, in place
+    Qi = Q.clone()
+    Y1, none = capi.qk_norm_rope3d(p, Qi, None, first=at, out_q=Qi)
+    assert none is None
+    check("Y", Y1, *norm(Q, None, cs, sn, p.eps)["Y"])
+    Gi = Gq.clone()
+    d1, _, w1, _ = capi.qk_norm_rope3d_backward(p, Q, None, None, None, Gi, None, first=at, out_q=Gi)
+    ref = norm(Q, None, cs, sn, p.eps, Gq)
+    check("dX", d1, *ref["dX"])
+    check("dw", w1, *ref["dw"])
+
+
+def test_qk_norm_rope3d_rows_of_zeros():
+    p = _norm_params("f32", N=9)
+    Q = torch.zeros((1, 2, 9, 64), device="cuda")
+    G = torch.ones_like(Q)
+    Y, _ = capi.qk_norm_rope3d(p, Q, None)
+    dQ, _, dw, _ = capi.qk_norm_rope3d_backward(p, Q, None, None, None, G, None)
+    cs, sn = angles(p, [0])
+    ref = norm(Q, None, cs, sn, p.eps, G)
+    assert (Y == 0).all() and (dw == 0).all()
+    check("dX", dQ, *ref["dX"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_qk_norm_rope3d_strided(dtype):
+    """From slices of a [B, N, 3, H, d] projection to dense [B, H, N, d], and back into the
+    slices of its gradient."""
+    p = _norm_params(dtype, B=2, H=3, N=91, split=(44, 42, 42))
+    dt = DT[dtype][0]
+    qkv = _randn((2, 91, 3, 3, 128), dt, 7)
+    Q, K = qkv[:, :, 0].transpose(1, 2), qkv[:, :, 1].transpose(1, 2)
+    Yq, Yk = capi.qk_norm_rope3d(p, Q, K)
+    Dq, Dk = capi.qk_norm_rope3d(p, Q.contiguous(), K.contiguous())
+    assert torch.equal(Yq, Dq) and torch.equal(Yk, Dk) and Yq.is_contiguous()
+    G = _randn(Yq.shape, dt, 8)
+    grad = torch.zeros_like(qkv)
+    out_q, out_k = grad[:, :, 0].transpose(1, 2), grad[:, :, 1].transpose(1, 2)
+    capi.qk_norm_rope3d_backward(p, Q, K, None, None, G, G, out_q=out_q, out_k=out_k)
+    dQ, dK, _, _ = capi.qk_norm_rope3d_backward(p, Q.contiguous(), K.contiguous(), None, None, G, G)
+    assert torch.equal(out_q, dQ) and torch.equal(out_k, dK) and (grad[:, :, 2] == 0).all()
+
+
+def test_qk_norm_rope3d_gradients_against_differences():
+    p = _norm_params("f32", N=40, first=17)
+    Q, G = _randn((1, 2, 40, 64), torch.float32, 9), _randn((1, 2, 40, 64), torch.float32, 10)
+    w = 1 + 0.2 * _randn((64,), torch.float32, 11)
+    cs, sn = angles(p, [17])
+    dQ, _, dw, _ = capi.qk_norm_rope3d_backward(p, Q, None, w, None, G, None)
+    f = lambda x, v: (norm(x, v, cs, sn, p.eps)["Y"][0] * G.double()).sum().item()  # noqa: E731
+    x, v, h = Q.double(), w.double(), 1e-5
+    e, ew = _randn(Q.shape, torch.float32, 12).double(), _randn((64,), torch.float32, 13).double()
+    num = (f(x + h * e, v) - f(x - h * e, v)) / (2 * h)
+    assert abs(num - (dQ.double() * e).sum().item()) <= 1e-5 * (dQ.double() * e).abs().sum().item()
+    num = (f(x, v + h * ew) - f(x, v - h * ew)) / (2 * h)
+    assert abs(num - (dw.double() * ew).sum().item()) <= 1e-5 * (dw.double() * ew).abs().sum().item()
+
+
+# ------------------------------------------------------------------------------ together
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_rope_window_attention_train_step(dtype):
+    """One layer as a model runs it: projection slices -> norm + RoPE -> window attention, and
+    the whole way back, against the chain of the binary64 forms' gradients (by autograd)."""
+    B, T, Hg, Wg, H, d = 2, 4, 5, 9, 3, 64
+    N = T * Hg * Wg
+    np_ = _norm_params(dtype, B=B, H=H, N=N, Hg=Hg, Wg=Wg)
+    wp = _params(dtype, B=B, H=H, Nq=N, d=d, frame=Hg * Wg, left=1, right=0, sinks=1)
+    dt = DT[dtype][0]
+    qkv = _randn((B, N, 3, H, d), dt, 21)
+    wq, wk = 1 + 0.2 * _randn((d,), torch.float32, 22), 1 + 0.2 * _randn((d,), torch.float32, 23)
+    G = _randn((B, H, N, d), dt, 24)
+    Q, K, V = (qkv[:, :, i].transpose(1, 2) for i in range(3))
+    Yq, Yk = capi.qk_norm_rope3d(np_, Q, K, wq, wk)
+    O, lse = capi.window_attention(wp, Yq, Yk, V, lse=True)
+    grad = torch.empty_like(qkv)
+    gq, gk, gv = (grad[:, :, i].transpose(1, 2) for i in range(3))
+    dYq, dYk = torch.empty_like(Yq), torch.empty_like(Yk)
+    capi.window_attention_backward(wp, Yq, Yk, V, O, G, lse, out=(dYq, dYk, gv))
+    _, _, dwq, dwk = capi.qk_norm_rope3d_backward(np_, Q, K, wq, wk, dYq, dYk, out_q=gq, out_k=gk)
+    torch.cuda.synchronize()
+
+    x = qkv.double().requires_grad_()
+    a, b = wq.double().requires_grad_(), wk.double().requires_grad_()
+    cs, sn = angles(np_, [0] * B)
+    q, k, v = (x[:, :, i].transpose(1, 2) for i in range(3))
+    yq, yk = norm(q, a, cs, sn, np_.eps)["Y"][0], norm(k, b, cs, sn, np_.eps)["Y"][0]
+    vis = visible(wp, [0] * B, [N] * B).cuda()[:, None]
+    s = (yq @ yk.mT / math.sqrt(d)).masked_fill(~vis, -math.inf)
+    o = torch.softmax(s, -1) @ v
+    (o * G.double()).sum().backward()
+    # each stage rounds to the type once (the gradients twice more on the way): relative
+    # 2-norm error of a few half steps
+    tol = 6 * 2.0 ** -8 if dtype == "bf16" else 2e-5
+    for n, got, want in (("O", O, o), ("dqkv", grad, x.grad), ("dwq", dwq, a.grad), ("dwk", dwk, b.grad)):
+        rel = ((got.double() - want).norm() / want.norm()).item()
+        assert rel <= tol, (n, rel)

@@ -1,0 +1,140 @@
+"""Refusals of the query/key norm and window attention entry points: no GPU, nothing launched."""
+import ctypes
+
+import pytest
+import torch
+
+from free_sparse_attention_b200 import capi
+from free_sparse_attention_b200.build import build
+
+FAKE = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def L():
+    build()
+    return capi.lib()
+
+
+def _norm(**over):
+    kw = dict(B=2, H=4, Hkv=2, N=30, d=64, d_t=16, d_h=24, d_w=24, Hg=3, Wg=5, first=0, eps=1e-6, base=1e4, dtype=1)
+    kw.update(over)
+    return capi.QkNormParams(**kw)
+
+
+def _window(**over):
+    kw = dict(B=2, H=4, Hkv=2, Nq=30, Nk=40, d=64, frame=1, left=5, right=0, sinks=1, q_first=10, dtype=1)
+    kw.update(over)
+    return capi.WindowParams(**kw)
+
+
+NORM_BAD = [(dict(B=0), 1), (dict(H=0), 1), (dict(Hkv=0), 1), (dict(N=0), 1), (dict(Hg=0), 1), (dict(Wg=-1), 1),
+            (dict(d_t=17, d_h=23), 1), (dict(d_t=18), 1), (dict(d_t=-16, d_h=56), 1), (dict(eps=-1.0), 1),
+            (dict(eps=float("nan")), 1), (dict(base=0.0), 1), (dict(base=float("inf")), 1), (dict(dtype=2), 1),
+            (dict(first=-1), 1), (dict(d=96, d_t=32, d_h=32, d_w=32), 2), (dict(N=(1 << 24) + 1), 2),
+            (dict(B=1 << 10, H=1 << 11), 2), (dict(B=16, N=1 << 24, H=8), 2), (dict(first=(1 << 30) + 1), 2)]
+
+
+@pytest.mark.parametrize("over,code", NORM_BAD)
+def test_norm_parameters_refused(L, over, code):
+    p = _norm(**over)
+    assert L.scope_qk_norm_workspace_bytes(ctypes.byref(p)) == 0
+    assert L.scope_qk_norm_rope3d(ctypes.byref(p), None, FAKE, FAKE, None, None, None, FAKE, FAKE, None) == code
+    assert L.scope_qk_norm_rope3d_backward(ctypes.byref(p), None, FAKE, FAKE, None, None, FAKE, FAKE, None, FAKE, FAKE,
+                                           FAKE, FAKE, FAKE, 1 << 30, None) == code
+
+
+def test_norm_pointers_refused(L):
+    p = ctypes.byref(_norm())
+    f = L.scope_qk_norm_rope3d
+    assert f(None, None, FAKE, FAKE, None, None, None, FAKE, FAKE, None) == 1
+    assert f(p, None, None, FAKE, None, None, None, FAKE, FAKE, None) == 1
+    assert f(p, None, FAKE, None, None, None, None, FAKE, FAKE, None) == 1        # keys out without keys in
+    assert f(p, None, FAKE, FAKE, None, None, None, FAKE, None, None) == 1
+    assert f(p, None, FAKE + 2, FAKE, None, None, None, FAKE, FAKE, None) == 1
+    assert f(p, None, FAKE, FAKE, FAKE + 4, None, None, FAKE, FAKE, None) == 1
+    assert f(p, None, FAKE, FAKE, None, None, FAKE + 4, FAKE, FAKE, None) == 1
+    g, need = L.scope_qk_norm_rope3d_backward, L.scope_qk_norm_workspace_bytes(p)
+    ok = [p, None, FAKE, FAKE, None, None, FAKE, FAKE, None, FAKE, FAKE, FAKE, FAKE, FAKE, need, None]
+    for i, v, code in ((13, None, 1), (13, FAKE + 16, 1), (14, need - 1, 3), (6, None, 1), (7, None, 1), (10, None, 1),
+                       (9, None, 1), (3, None, 1), (11, FAKE + 8, 1)):
+        bad = list(ok)
+        bad[i] = v
+        assert g(*bad) == code, (i, v)
+
+
+WINDOW_BAD = [(dict(B=0), 1), (dict(H=0), 1), (dict(Hkv=0), 1), (dict(Hkv=3), 1), (dict(Nq=0), 1), (dict(Nk=0), 1),
+              (dict(frame=0), 1), (dict(left=-2), 1), (dict(right=-2), 1), (dict(sinks=-1), 1), (dict(q_first=-1), 1),
+              (dict(dtype=5), 1), (dict(d=96), 2), (dict(Nq=(1 << 24) + 1), 2), (dict(Nk=(1 << 24) + 1), 2),
+              (dict(frame=(1 << 24) + 1), 2), (dict(left=(1 << 30) + 1), 2), (dict(sinks=(1 << 30) + 1), 2),
+              (dict(q_first=(1 << 30) + 1), 2), (dict(B=1 << 11, H=1 << 10), 2), (dict(Nq=1 << 24, H=128, Hkv=128), 2)]
+
+
+@pytest.mark.parametrize("over,code", WINDOW_BAD)
+def test_window_parameters_refused(L, over, code):
+    p = _window(**over)
+    assert L.scope_window_workspace_bytes(ctypes.byref(p)) == 0
+    assert L.scope_window_attention(ctypes.byref(p), None, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, 1 << 40,
+                                    None) == code
+    assert L.scope_window_attention_backward(ctypes.byref(p), None, *[FAKE] * 6, None, None, *[FAKE] * 4, 1 << 40,
+                                             None) == code
+
+
+def test_window_pointers_refused(L):
+    p = ctypes.byref(_window())
+    need = L.scope_window_workspace_bytes(p)
+    ok = [p, None, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, need, None]
+    for i, v, code in ((0, None, 1), (2, None, 1), (3, None, 1), (4, None, 1), (7, None, 1), (9, None, 1),
+                       (9, FAKE + 128, 1), (10, need - 1, 3), (3, FAKE + 8, 1), (5, FAKE + 4, 1), (6, FAKE + 4, 1),
+                       (8, FAKE + 4, 1)):
+        bad = list(ok)
+        bad[i] = v
+        assert L.scope_window_attention(*bad) == code, (i, v)
+    ok = [p, None] + [FAKE] * 6 + [None, None] + [FAKE] * 4 + [need, None]
+    for i, v, code in ((0, None, 1), (5, None, 1), (6, None, 1), (7, None, 1), (10, None, 1), (11, None, 1),
+                       (12, None, 1), (13, None, 1), (14, need - 1, 3), (12, FAKE + 2, 1)):
+        bad = list(ok)
+        bad[i] = v
+        assert L.scope_window_attention_backward(*bad) == code, (i, v)
+
+
+@pytest.mark.parametrize("strides", [(0, 0, 64), (7680, 1920, 60), (7680, 1920, 68), (-7680, 1920, 64), (7680, 1856, 64),
+                                     (100, 1920, 64), (7680, 0, 64), (7680, 64, 64), (1 << 50, 1920, 64)])
+def test_layouts_refused(L, strides):
+    """Zero or negative strides of a dimension longer than one, strides that are no multiple of
+    16 bytes, and layouts in which two elements share a place."""
+    p, lay = _window(), capi.WindowLayouts()
+    lay.q = capi.Strides(*strides)
+    need = L.scope_window_workspace_bytes(ctypes.byref(p))
+    assert L.scope_window_attention(ctypes.byref(p), ctypes.byref(lay), FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE,
+                                    need, None) == 1
+    q, lay = _norm(), capi.QkNormLayouts()
+    lay.yk = capi.Strides(*strides)
+    assert L.scope_qk_norm_rope3d(ctypes.byref(q), ctypes.byref(lay), FAKE, FAKE, None, None, None, FAKE, FAKE, None) == 1
+
+
+def test_workspace_sizes(L):
+    size = lambda **o: L.scope_window_workspace_bytes(ctypes.byref(_window(**o)))  # noqa: E731
+    assert size() % 256 == 0 and size() > 0
+    # few rows over a long cache: room for the shares of every row
+    assert size(Nq=1, Nk=1 << 20, left=-1) >= 2 * 4 * 2 * 64 * 4
+    assert L.scope_qk_norm_workspace_bytes(ctypes.byref(_norm())) % 256 == 0
+    with pytest.raises(capi.ScopeError):
+        capi.alloc_window_workspace(_window(d=96))
+    with pytest.raises(capi.ScopeError):
+        capi.alloc_qk_norm_workspace(_norm(N=0))
+
+
+def test_binding_refuses_tensors_that_do_not_fit():
+    """Shapes, types, devices and channel strides are checked before the library is called."""
+    p = _window()
+    Q, K = torch.zeros((2, 4, 30, 64)), torch.zeros((2, 2, 40, 64))
+    for args in ((Q, K, K), (Q.bfloat16(), K.bfloat16(), K.bfloat16())):      # float32; not on a GPU
+        with pytest.raises(ValueError):
+            capi._tensors("f", p, capi.WindowLayouts, (("q", args[0], (2, 4, 30, 64)), ("k", args[1], (2, 2, 40, 64))))
+    with pytest.raises(ValueError):
+        capi._vector("f", "k_len", torch.zeros(3, dtype=torch.int32), 2, torch.int32, torch.device("cpu"))
+    with pytest.raises(ValueError):
+        capi._vector("f", "k_len", torch.zeros(2, dtype=torch.int64), 2, torch.int32, torch.device("cpu"))
+    with pytest.raises(ValueError):
+        capi._workspace("f", torch.zeros(4, dtype=torch.float32), torch.device("cpu"))
