@@ -89,6 +89,57 @@ __device__ __forceinline__ bool warp_aborted(volatile int *abort_flag)
     return __any_sync(0xffffffffu, *abort_flag != 0);
 }
 
+// Waits of a kernel whose limit is a launch argument.
+struct Waiter {
+    volatile int *abort_flag;
+    int32_t *status;
+    unsigned long long limit_ns;
+};
+
+// Bounded wait by one thread (as bar_wait, with the launch's limit).
+__device__ __forceinline__ bool wait1(uint64_t *b, uint32_t parity, const Waiter &w)
+{
+    if (bar_test(b, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    unsigned ns = 8;
+    while (!bar_test(b, parity)) {
+        __nanosleep(ns);
+        ns = ns < 64 ? ns * 2 : 64;
+        if (*w.abort_flag) return false;
+        if (global_ns() - t0 > w.limit_ns) {
+            *w.abort_flag = 1;
+            set_status(w.status, SCOPE_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// Warp-uniform wait: lane 0 polls, every lane gets the same answer.
+__device__ __forceinline__ bool waitw(uint64_t *b, uint32_t parity, const Waiter &w)
+{
+    int ok = 0;
+    if ((threadIdx.x & 31) == 0) ok = wait1(b, parity, w) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+
+// A wait with no abort check, for draining work already issued (bounded all the same).
+__device__ __forceinline__ void drain_wait(uint64_t *b, uint32_t parity, unsigned long long limit_ns)
+{
+    const unsigned long long t0 = global_ns();
+    while (!bar_test(b, parity) && global_ns() - t0 < limit_ns) __nanosleep(64);
+}
+
+// max(a, b, c) in one instruction (the three-input form of max.f32 on sm_100)
+__device__ __forceinline__ float fmax3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ void bar_expect_tx(uint64_t *b, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], %0;" ::"r"(bytes), "r"(smem_u32(b))

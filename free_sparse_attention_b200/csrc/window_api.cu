@@ -158,17 +158,18 @@ Plan plan_of(const scope_window_params &p)
     const int G = p.H / p.Hkv;
     // few rows: the query heads of one key head share a tile, so that its keys are read once
     r.pack = (long long)G * p.Nq <= 16 ? G : 1;
-    const int bm = (long long)r.pack * p.Nq <= 16 ? 16 : 64;
+    // rows of one item: 16 (few rows), 256 (tensor cores) or 64 (fp32)
+    const int bm = (long long)r.pack * p.Nq <= 16 ? 16 : (p.dtype == SCOPE_BF16 ? 256 : 64);
     const long long rows = (long long)r.pack * p.Nq, tiles = (rows + bm - 1) / bm;
     const long long items = (long long)p.B * (p.H / r.pack) * tiles;
     // keys of one item, at most
     const long long left = p.left < 0 ? kWinUnbounded : p.left, right = p.right < 0 ? kWinUnbounded : p.right;
     const long long span = std::min((long long)p.Nk, (left + right + 1 + p.sinks) * p.frame + bm);
     const long long key_tiles = (span + 63) / 64;
-    // four items per SM, shares of at least two key tiles
-    long long splits = (4ll * kPlanSms + items - 1) / items;
-    splits = std::min(splits, std::max(1ll, key_tiles / 2));
-    r.splits = items >= 2 * kPlanSms ? 1 : (int)std::min<long long>(std::max(1ll, splits), kMaxSplits);
+    // four items per SM (one where an item takes a whole SM), shares of at least two key tiles
+    const long long want = (bm == 256 ? 1ll : 4ll) * kPlanSms;
+    const long long splits = std::min(want / items, std::max(1ll, key_tiles / 2));
+    r.splits = (int)std::min<long long>(std::max(1ll, splits), kMaxSplits);
     return r;
 }
 
@@ -330,7 +331,8 @@ scope_status scope_window_attention(const scope_window_params *p, const scope_wi
     a.O = O;
     a.lse = lse;
     if (cudaMemsetAsync(ws, 0, kHeader, s) != cudaSuccess) return SCOPE_ERR_CUDA;
-    cudaError_t e = window_simt_forward(a, s);
+    const bool tc = a.is_bf16 && (long long)a.pack * a.Nq > 16;
+    cudaError_t e = tc ? window_tc_forward(a, s) : window_simt_forward(a, s);
     if (e == cudaSuccess && a.splits > 1) e = window_join(a, s);
     return cuda_status(e);
 }
