@@ -362,6 +362,7 @@ scope_status scope_window_attention_backward(const scope_window_params *p, const
     a.dQ = dQ;
     a.dK = dK;
     a.dV = dV;
+    if (a.is_bf16) return cuda_status(window_tc_backward(a, s));
     if (cudaMemsetAsync(ws, 0, kHeader, s) != cudaSuccess) return SCOPE_ERR_CUDA;
     return cuda_status(window_simt_backward(a, s));
 }

@@ -1,0 +1,591 @@
+// Window attention with sinks on the Blackwell tensor cores (tcgen05, sm_100a): the bf16
+// gradients.
+//
+// With P = 2^(c Q K^T - lse), D_i = dO_i . O_i and dS = P o (dO V^T - D):
+//   dQ = dS K / sqrt d,  dK = dS^T Q / sqrt d,  dV = P^T dO.
+// Two kernels of one shape, so that every sum has one owner and a fixed order (no atomics, no
+// fp32 gradient in memory; S and dO V^T are computed in both, 7 products instead of 5).  A CTA
+// owns 128 rows and walks column tiles of 64:
+//            rows R1, R2   columns C1, C2   S = R1 C1^T  dP = R2 C2^T   results
+//   dQ       Q, dO         K, V             S            dP             dQ += dS C1
+//   dK, dV   K, V          Q, dO            S^T          dP^T           dK += dS C1, dV += P C2
+// Per CTA (persistent, one per SM): warps 0-3 / 4-7 turn S and dP of even / odd steps into P and
+// dS (thread r owns row r = TMEM lane r); warp 8 loads rows and column tiles by TMA and hands out
+// the items; warp 9 stages lse and D of the columns (dK, dV); warp 10 issues S and dP of a step
+// (two buffers, so it runs up to two steps ahead); warp 11 issues the products of P and dS, read
+// from TMEM where they replace S and dP.  P and dS are rounded to bf16 once, as operands;
+// everything summed is fp32.
+#include "window_tc.cuh"
+
+namespace scope {
+
+namespace {
+
+constexpr int kBM = 128, kBN = 64;
+constexpr int kWarps = 12, kThreads = kWarps * 32;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "register split");
+constexpr int kMaxStages = 6, kRing = 4;
+constexpr uint32_t kTmemCols = 512;
+
+struct __align__(8) Bars {
+    uint64_t r_full, r_empty, land, out_full, out_free;
+    uint64_t c_full[kMaxStages], c_empty[kMaxStages], ls_full[kMaxStages];
+    uint64_t s_full[2], p_full[2], buf_free[2], drain[2];
+    uint64_t item_full[kRing], item_empty[kRing];
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kRows = kBM * D * 2, kTile = kBN * D * 2;
+    static constexpr int kR1 = 0, kR2 = kRows, kC = 2 * kRows;               // stage s: C1, C2
+    static constexpr int kLs = kC + kStages * 2 * kTile;                     // stage s: lse [64], D [64]
+    static constexpr int kBars = kLs + kStages * 2 * kBN * 4;
+    static constexpr int kMisc = kBars + (int)sizeof(Bars);
+    static constexpr int kAlloc = kMisc + 64 + 1024;
+    static_assert(kAlloc <= 232448, "shared memory budget");
+    static_assert(kAlloc > 232448 / 2, "one CTA (and its 512 TMEM columns) per SM");
+};
+
+// One item: 128 rows of one head, and its column tiles in order.
+template <bool DKV>
+struct Item {
+    int b, h, r0, nrows;   // h: query head (dQ) or key head (dK, dV)
+    int first, kl;
+    WinRow a, z;           // dQ: limits of the first and last row
+    WinTiles wt;           // dQ: key tiles
+    int c0, per, steps;    // dK, dV: first query tile and tiles per query head; column tiles in all
+};
+
+template <bool DKV>
+__device__ __forceinline__ Item<DKV> item_of(const WinArgs &a, int it)
+{
+    Item<DKV> x;
+    const int n = DKV ? a.Nk : a.Nq, heads = DKV ? a.Hkv : a.H, tiles = (n + kBM - 1) / kBM;
+    int bh, tile;
+    if (DKV) {
+        // sink tiles meet every later query: those of all heads first; then head by head
+        const int units = a.B * heads;
+        const int sink = (int)min((long long)tiles, ((long long)a.sinks * a.frame + kBM - 1) / kBM);
+        if (it < units * sink) {
+            tile = it / units;
+            bh = it % units;
+        } else {
+            it -= units * sink;
+            bh = it / (tiles - sink);
+            tile = sink + it % (tiles - sink);
+        }
+    } else {
+        bh = it / tiles;
+        tile = tiles - 1 - it % tiles;
+    }
+    x.b = bh / heads;
+    x.h = bh % heads;
+    x.r0 = tile * kBM;
+    x.nrows = min(kBM, n - x.r0);
+    x.first = win_first(a, x.b);
+    x.kl = win_klen(a, x.b);
+    if (DKV) {
+        const int2 qr = win_queries(a, x.first, x.kl, a.Nq, x.r0, x.r0 + x.nrows);
+        x.c0 = qr.x / kBN;
+        x.per = qr.y > qr.x ? (qr.y + kBN - 1) / kBN - x.c0 : 0;
+        x.steps = x.per * (a.H / a.Hkv);
+    } else {
+        x.a = win_row(a, x.first + x.r0, x.kl);
+        x.z = win_row(a, x.first + x.r0 + x.nrows - 1, x.kl);
+        x.wt = win_tiles<kBN>(x.a, x.z);
+        x.steps = x.wt.count();
+    }
+    return x;
+}
+
+// Column tile t of an item: head and first column.
+template <bool DKV>
+__device__ __forceinline__ int2 column_of(const WinArgs &a, const Item<DKV> &x, int t)
+{
+    if (DKV) return make_int2(x.h * (a.H / a.Hkv) + t / x.per, (x.c0 + t % x.per) * kBN);
+    return make_int2(x.h / (a.H / a.Hkv), x.wt.at(t) * kBN);
+}
+
+template <bool DKV, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmR1, const __grid_constant__ CUtensorMap tmR2,
+                         const __grid_constant__ CUtensorMap tmC1, const __grid_constant__ CUtensorMap tmC2,
+                         const __grid_constant__ WinArgs a, int n_items)
+{
+    using L = Smem<D>;
+    constexpr int NB = D / 64, NS = L::kStages;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars *bars = reinterpret_cast<Bars *>(sm + L::kBars);
+    int *misc = reinterpret_cast<int *>(sm + L::kMisc);
+    volatile int *abort_flag = misc;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 1);
+    volatile int *ring = misc + 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sbase = smem_u32(sm);
+    const Waiter W{abort_flag, a.status, a.wait_ns};
+    int32_t *counter = a.counter + (DKV ? 1 : 0);
+
+    if (threadIdx.x == 0) {
+        misc[0] = 0;
+        bar_init(&bars->r_full, 1);
+        bar_init(&bars->r_empty, 1);
+        bar_init(&bars->land, 1);
+        bar_init(&bars->out_full, 1);
+        bar_init(&bars->out_free, 8);
+        for (int s = 0; s < kMaxStages; ++s) {
+            bar_init(&bars->c_full[s], 1);
+            bar_init(&bars->c_empty[s], 1);
+            bar_init(&bars->ls_full[s], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            bar_init(&bars->s_full[w], 1);
+            bar_init(&bars->p_full[w], 4);
+            bar_init(&bars->buf_free[w], 1);
+            bar_init(&bars->drain[w], 1);
+        }
+        for (int k = 0; k < kRing; ++k) {
+            bar_init(&bars->item_full[k], 1);
+            bar_init(&bars->item_empty[k], kWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 10) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // TMEM columns: buffer w: S at 128 w, dP at 128 w + 64 (P, dS as bf16 pairs over the first 32
+    // of each); out1 (dQ or dK) at 256, out2 (dV) at 256 + D
+    const uint32_t out1 = tmem + 256, out2 = tmem + 256 + D;
+    auto fetch = [&](uint32_t k) -> bool {   // lane 0 of warp 8: the item scheduler
+        const int slot = k % kRing;
+        if (!wait1(&bars->item_empty[slot], ((k / kRing) & 1) ^ 1, W)) return false;
+        const int it = atomicAdd(counter, 1);
+        ring[slot] = it < n_items ? it : -1;
+        bar_arrive(&bars->item_full[slot]);
+        return true;
+    };
+    auto next_item = [&](uint32_t k) -> int {
+        const int slot = k % kRing;
+        if (!waitw(&bars->item_full[slot], (k / kRing) & 1, W)) return -1;
+        const int it = ring[slot];
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bars->item_empty[slot]);
+        if (warp == 8 && it >= 0) {
+            int ok = 1;
+            if (lane == 0) ok = fetch(k + 1) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) return -1;
+        }
+        return it;
+    };
+    if (warp == 8 && lane == 0) fetch(0);
+
+    // Every role counts the CTA's steps in g: step g uses buffer g % 2 (use g / 2) and column
+    // stage g % NS (use g / NS).
+    uint32_t g = 0;
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8) {
+            // ------------------------------------------------------------------ loads
+            uint32_t r_it = 0, land = 0;
+            bool landing = false;
+            for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
+                const int it = next_item(item_k);
+                if (it < 0) break;
+                const Item<DKV> x = item_of<DKV>(a, it);
+                if (x.steps == 0) continue;
+                int ok = 1;
+                if (lane == 0) {
+                    ok = wait1(&bars->r_empty, (r_it & 1) ^ 1, W);
+                    if (ok) {
+                        bar_expect_tx(&bars->r_full, 2 * L::kRows);
+#pragma unroll
+                        for (int k = 0; k < NB; ++k) {
+                            tma_rows(sbase + L::kR1 + k * (kBM * 128), &tmR1, k * 64, x.r0, x.h, x.b, &bars->r_full);
+                            tma_rows(sbase + L::kR2 + k * (kBM * 128), &tmR2, k * 64, x.r0, x.h, x.b, &bars->r_full);
+                        }
+                        ++r_it;
+                    }
+                }
+                for (int t = 0; t < x.steps; ++t) {
+                    const int s = g % NS;
+                    const int2 col = column_of<DKV>(a, x, t);
+                    // dQ: key rows that no row of the item sees are zeroed (0 x NaN would reach dQ)
+                    const bool whole = DKV || col.y + kBN <= x.a.s || (col.y >= x.a.lo && col.y + kBN <= x.z.hi);
+                    if (lane == 0 && ok) {
+                        ok = wait1(&bars->c_empty[s], ((g / NS) & 1) ^ 1, W);
+                        if (ok) {
+                            uint64_t *bar = whole ? &bars->c_full[s] : &bars->land;
+                            bar_expect_tx(bar, 2 * L::kTile);
+                            const uint32_t dst = sbase + L::kC + s * 2 * L::kTile;
+#pragma unroll
+                            for (int k = 0; k < NB; ++k) {
+                                tma_rows(dst + k * (kBN * 128), &tmC1, k * 64, col.y, col.x, x.b, bar);
+                                tma_rows(dst + L::kTile + k * (kBN * 128), &tmC2, k * 64, col.y, col.x, x.b, bar);
+                            }
+                            if (!whole) {
+                                landing = true;
+                                ok = wait1(&bars->land, land & 1, W);
+                                landing = !ok;
+                            }
+                        }
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    if constexpr (!DKV) {
+                        __syncwarp();
+                        if (!whole) {
+                            ++land;
+                            for (int e = lane; e < kBN * NB * 8; e += 32) {
+                                const int r = e / (NB * 8), j = col.y + r;
+                                if (!(j < x.a.s || (j >= x.a.lo && j < x.z.hi)))
+                                    *reinterpret_cast<uint4 *>(sm + L::kC + s * 2 * L::kTile + (e / 8 % NB) * (kBN * 128) +
+                                                               r * 128 + (e % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(&bars->c_full[s]);
+                        }
+                    }
+                    ++g;
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+            }
+            if (lane == 0) {   // copies already issued land before the CTA exits
+                for (uint32_t v = g > (uint32_t)NS ? g - NS : 0; v < g; ++v)
+                    drain_wait(&bars->c_full[v % NS], (v / NS) & 1, W.limit_ns);
+                if (landing) drain_wait(&bars->land, land & 1, W.limit_ns);
+                if (r_it > 0) drain_wait(&bars->r_full, (r_it - 1) & 1, W.limit_ns);
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ------------------------------------------------------------------ lse and D of the columns
+            for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
+                const int it = next_item(item_k);
+                if (it < 0) break;
+                if constexpr (DKV) {
+                    const Item<DKV> x = item_of<DKV>(a, it);
+                    bool ok = true;
+                    for (int t = 0; t < x.steps; ++t) {
+                        const int s = g % NS;
+                        const int2 col = column_of<DKV>(a, x, t);
+                        const long long row = win_row_index(a, x.b, col.x, col.y);
+                        float v[4];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int e = lane + 32 * k;
+                            const bool in = col.y + e < a.Nq;
+                            v[k] = in ? a.lse[row + e] * -1.4426950408889634f : 0.f;
+                            v[2 + k] = in ? -a.delta[row + e] : 0.f;
+                        }
+                        ok = waitw(&bars->c_empty[s], ((g / NS) & 1) ^ 1, W);
+                        if (!ok) break;
+                        float *ls = reinterpret_cast<float *>(sm + L::kLs) + s * 2 * kBN;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            ls[lane + 32 * k] = v[k];
+                            ls[kBN + lane + 32 * k] = v[2 + k];
+                        }
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&bars->ls_full[s]);
+                        ++g;
+                    }
+                    if (!ok) break;
+                }
+            }
+        } else if (lane == 0) {
+            // ------------------------------------------------------------------ product issuers
+            constexpr uint32_t idesc_s = f16_idesc(kBM, kBN, false), idesc_o = f16_idesc(kBM, D, true);
+            const bool first_products = warp == 10;
+            const uint64_t r1 = sw128_desc(sbase + L::kR1, 16, 1024), r2 = sw128_desc(sbase + L::kR2, 16, 1024);
+            uint32_t items = 0;
+            bool issued = false;
+            for (uint32_t item_k = 0; !*abort_flag; ++item_k) {
+                const int slot = item_k % kRing;
+                if (!wait1(&bars->item_full[slot], (item_k / kRing) & 1, W)) break;
+                const int it = ring[slot];
+                bar_arrive(&bars->item_empty[slot]);
+                if (it < 0) break;
+                const int steps = item_of<DKV>(a, it).steps;
+                if (steps == 0) continue;
+                bool ok = true;
+                issued = true;
+                if (first_products) {
+                    ok = wait1(&bars->r_full, items & 1, W);
+                    for (int t = 0; t < steps && ok; ++t, ++g) {
+                        const int s = g % NS, w = g & 1;
+                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W) && wait1(&bars->buf_free[w], ((g >> 1) & 1) ^ 1, W);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t cb = sbase + L::kC + s * 2 * L::kTile;
+                        const uint64_t c1 = sw128_desc(cb, 16, 1024), c2 = sw128_desc(cb + L::kTile, 16, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t offa = (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
+                            const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
+                            mma_bf16(tmem + 128 * w, r1 + offa, c1 + offb, idesc_s, kk > 0);
+                        }
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t offa = (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
+                            const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
+                            mma_bf16(tmem + 128 * w + 64, r2 + offa, c2 + offb, idesc_s, kk > 0);
+                        }
+                        mma_commit(&bars->s_full[w]);
+                        if (t == steps - 1) mma_commit(&bars->r_empty);
+                    }
+                } else {
+                    for (int t = 0; t < steps && ok; ++t, ++g) {
+                        const int s = g % NS, w = g & 1;
+                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W) && wait1(&bars->p_full[w], (g >> 1) & 1, W);
+                        if (ok && t == 0) ok = wait1(&bars->out_free, (items & 1) ^ 1, W);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t cb = sbase + L::kC + s * 2 * L::kTile;
+                        const uint64_t c1 = sw128_desc(cb, kBN * 128, 1024), c2 = sw128_desc(cb + L::kTile, kBN * 128, 1024);
+                        if constexpr (DKV) {
+#pragma unroll
+                            for (int kk = 0; kk < kBN / 16; ++kk)
+                                mma_bf16_ts(out2, tmem + 128 * w + kk * 8, c2 + (uint64_t)(kk * 2048 >> 4), idesc_o,
+                                            (t > 0 || kk > 0) ? 1u : 0u);
+                        }
+#pragma unroll
+                        for (int kk = 0; kk < kBN / 16; ++kk)
+                            mma_bf16_ts(out1, tmem + 128 * w + 64 + kk * 8, c1 + (uint64_t)(kk * 2048 >> 4), idesc_o,
+                                        (t > 0 || kk > 0) ? 1u : 0u);
+                        mma_commit(&bars->buf_free[w]);
+                        mma_commit(&bars->c_empty[s]);
+                        if (t == steps - 1) mma_commit(&bars->out_full);
+                    }
+                }
+                if (!ok) break;
+                ++items;
+            }
+            if (issued) {   // every product issued completes before TMEM is freed
+                mma_commit(&bars->drain[warp - 10]);
+                drain_wait(&bars->drain[warp - 10], 0, W.limit_ns);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------------- P and dS, epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int wg = warp >> 2, row = threadIdx.x - wg * kBM;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        uint32_t items = 0;
+        for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
+            const int it = next_item(item_k);
+            if (it < 0) break;
+            const Item<DKV> x = item_of<DKV>(a, it);
+            const bool valid = row < x.nrows;
+            // what the row sees: columns [0, s) and [lo, hi) (dQ) or [lo, hi) (dK, dV)
+            WinRow lim{0, 0, 0};
+            float nlse = 0.f, ndelta = 0.f;
+            if (valid) {
+                if constexpr (DKV) {
+                    const int2 qr = win_queries(a, x.first, x.kl, a.Nq, x.r0 + row, x.r0 + row + 1);
+                    lim.lo = qr.x;
+                    lim.hi = qr.y;
+                } else {
+                    lim = win_row(a, x.first + x.r0 + row, x.kl);
+                    const long long ix = win_row_index(a, x.b, x.h, x.r0 + row);
+                    nlse = a.lse[ix] * -1.4426950408889634f;
+                    ndelta = -a.delta[ix];
+                }
+            }
+            const unsigned long long c2 = f2pack(a.scale_log2, a.scale_log2);
+            bool ok = true;
+            for (int t = 0; t < x.steps; ++t, ++g) {
+                if ((int)(g & 1) != wg) continue;
+                const int s = g % NS;
+                const int j0 = column_of<DKV>(a, x, t).y;
+                if constexpr (DKV) ok = waitw(&bars->ls_full[s], (g / NS) & 1, W);
+                ok = ok && waitw(&bars->s_full[wg], (g >> 1) & 1, W);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sb = tmem + lane_base + 128 * wg;
+                float sv[kBN], dv[kBN];
+                tmem_ld32(sb, sv);
+                tmem_ld32(sb + 64, dv);
+                tmem_ld32(sb + 32, sv + 32);
+                tmem_ld32(sb + 96, dv + 32);
+                auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
+                const unsigned long long vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
+                const bool whole = __all_sync(0xffffffffu, vis == ~0ull);
+                tmem_wait_ld();
+                const float *ls = reinterpret_cast<const float *>(sm + L::kLs) + s * 2 * kBN;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pp[16], pd[16];
+                    const uint32_t bits = (uint32_t)(vis >> (32 * h));
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float4 l4, d4;
+                        if constexpr (DKV) {
+                            l4 = *reinterpret_cast<const float4 *>(ls + 32 * h + 2 * e);
+                            d4 = *reinterpret_cast<const float4 *>(ls + kBN + 32 * h + 2 * e);
+                        } else {
+                            l4 = make_float4(nlse, nlse, nlse, nlse);
+                            d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j = 32 * h + 2 * (e + k);
+                            const float2 ex = f2unpack(f2fma(f2pack(sv[j], sv[j + 1]), c2,
+                                                             k ? f2pack(l4.z, l4.w) : f2pack(l4.x, l4.y)));
+                            float p0 = fast_exp2(ex.x), p1 = fast_exp2(ex.y);
+                            const float2 dd = f2unpack(f2add(f2pack(dv[j], dv[j + 1]),
+                                                             k ? f2pack(d4.z, d4.w) : f2pack(d4.x, d4.y)));
+                            float s0 = p0 * dd.x, s1 = p1 * dd.y;
+                            if (!whole) {
+                                const bool v0 = (bits >> (2 * (e + k))) & 1u, v1 = (bits >> (2 * (e + k) + 1)) & 1u;
+                                p0 = v0 ? p0 : 0.f;
+                                p1 = v1 ? p1 : 0.f;
+                                s0 = v0 ? s0 : 0.f;
+                                s1 = v1 ? s1 : 0.f;
+                            }
+                            __nv_bfloat162 q2 = __floats2bfloat162_rn(p0, p1), d2 = __floats2bfloat162_rn(s0, s1);
+                            pp[e + k] = *reinterpret_cast<uint32_t *>(&q2);
+                            pd[e + k] = *reinterpret_cast<uint32_t *>(&d2);
+                        }
+                    }
+                    if constexpr (DKV) tmem_st16(sb + h * 16, pp);
+                    tmem_st16(sb + 64 + h * 16, pd);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bars->p_full[wg]);
+            }
+            if (!ok) break;
+            // epilogue: dK by warpgroup 0 and dV by 1; of dQ, half the channels each
+            if (x.steps > 0) {
+                if (!waitw(&bars->out_full, items & 1, W)) break;
+                ++items;
+                tc_fence_after();
+            }
+            constexpr int CH = DKV ? D : D / 2;   // channels of one warpgroup
+            const uint32_t src = tmem + lane_base + (DKV ? 256 + wg * D : 256 + wg * CH);
+            const float scale = DKV && wg == 1 ? 1.f : a.scale;
+            const WinLayout lay = DKV ? (wg ? a.ldv : a.ldk) : a.ldq;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(DKV ? (wg ? a.dV : a.dK) : a.dQ) + x.b * lay.b + x.h * lay.h +
+                                 (x.r0 + row) * lay.n + (DKV ? 0 : wg * CH);
+#pragma unroll 1
+            for (int h = 0; h < CH / 32; ++h) {
+                float o[32];
+                if (x.steps > 0) {
+                    tmem_ld32(src + h * 32, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                if (!valid) continue;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        __nv_bfloat162 hh = __floats2bfloat162_rn(o[e + 2 * k] * scale, o[e + 2 * k + 1] * scale);
+                        pk[k] = *reinterpret_cast<uint32_t *>(&hh);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + h * 32 + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+            }
+            if (x.steps > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bars->out_free);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 10)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// D_i = dO_i . O_i, D / 8 threads per row; clears the status word and the item counters first
+// (this launch precedes the two kernels above on the stream).
+template <int D>
+__global__ void __launch_bounds__(256) window_delta_kernel(WinArgs a)
+{
+    constexpr int TPR = D / 8;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *a.status = 0;
+        a.counter[0] = a.counter[1] = 0;
+    }
+    const long long row = (long long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR, rows = (long long)a.B * a.H * a.Nq;
+    const int g = threadIdx.x % TPR;
+    float s = 0.f;
+    if (row < rows) {
+        const int i = (int)(row % a.Nq), h = (int)(row / a.Nq % a.H), b = (int)(row / a.Nq / a.H);
+        const uint4 o = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.O) + b * a.lo.b + h * a.lo.h +
+                                                         i * a.lo.n + 8 * g);
+        const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.G) + b * a.lg.b + h * a.lg.h +
+                                                         i * a.lg.n + 8 * g);
+        const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            s = fmaf(__uint_as_float(ow[k] << 16), __uint_as_float(gw[k] << 16), s);
+            s = fmaf(__uint_as_float(ow[k] & 0xFFFF0000u), __uint_as_float(gw[k] & 0xFFFF0000u), s);
+        }
+    }
+#pragma unroll
+    for (int x = TPR / 2; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    if (g == 0 && row < rows) a.delta[row] = s;
+}
+
+template <bool DKV, int D>
+cudaError_t launch_pass(const WinArgs &a, cudaStream_t s)
+{
+    CUtensorMap r1, r2, c1, c2;
+    const int rows = DKV ? kBN : kBM, keys = DKV ? kBM : kBN;   // rows of a query and of a key tile
+    CUtensorMap &q = DKV ? c1 : r1, &g = DKV ? c2 : r2, &k = DKV ? r1 : c1, &v = DKV ? r2 : c2;
+    if (!rows_map(&q, a.Q, a.lq, a.B, a.H, a.Nq, D, rows) || !rows_map(&g, a.G, a.lg, a.B, a.H, a.Nq, D, rows) ||
+        !rows_map(&k, a.K, a.lk, a.B, a.Hkv, a.Nk, D, keys) || !rows_map(&v, a.V, a.lv, a.B, a.Hkv, a.Nk, D, keys))
+        return cudaErrorInvalidValue;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, window_bwd_tc_kernel<DKV, D>) != cudaSuccess || fa.numRegs != kLaunchRegs)
+        return cudaErrorInvalidDeviceFunction;
+    const long long items = DKV ? (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM) : (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM);
+    if (items > 0x7ffffff0ll) return cudaErrorInvalidConfiguration;
+    const int smem = Smem<D>::kAlloc;
+    cudaError_t e = cudaFuncSetAttribute(window_bwd_tc_kernel<DKV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    window_bwd_tc_kernel<DKV, D><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(r1, r2, c1, c2, a,
+                                                                                                           (int)items);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t backward(const WinArgs &a, cudaStream_t s)
+{
+    const long long rows = (long long)a.B * a.H * a.Nq;
+    const int per = 256 / (D / 8);
+    window_delta_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_pass<false, D>(a, s);
+    if (e == cudaSuccess) e = launch_pass<true, D>(a, s);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t window_tc_backward(const WinArgs &a, cudaStream_t s)
+{
+    return a.d == 64 ? backward<64>(a, s) : backward<128>(a, s);
+}
+
+}  // namespace scope
