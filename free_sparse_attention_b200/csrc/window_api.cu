@@ -149,6 +149,7 @@ scope_status validate(const scope_window_params *p)
 // per row tile.  A function of the shape alone, so that the workspace and the order of every
 // sum are too.
 struct Plan {
+    bool few;
     int pack, splits;
 };
 
@@ -157,19 +158,31 @@ Plan plan_of(const scope_window_params &p)
     Plan r;
     const int G = p.H / p.Hkv;
     // few rows: the query heads of one key head share a tile, so that its keys are read once
-    r.pack = (long long)G * p.Nq <= 16 ? G : 1;
-    // rows of one item: 16 (few rows), 256 (tensor cores) or 64 (fp32)
-    const int bm = (long long)r.pack * p.Nq <= 16 ? 16 : (p.dtype == SCOPE_BF16 ? 256 : 64);
+    r.few = (long long)G * p.Nq <= 16;
+    r.pack = r.few ? G : 1;
+    // rows of one item and keys of one of its tiles: few rows, tensor cores, or fp32; items
+    // that the device holds at a time
+    const bool bf16 = p.dtype == SCOPE_BF16;
+    const int bm = r.few ? 16 : (bf16 ? 256 : 64), bn = r.few && bf16 ? 16 : 64;
+    const int slots = kPlanSms * (bf16 ? (r.few ? 2 : 1) : (r.few ? 3 : 1));
     const long long rows = (long long)r.pack * p.Nq, tiles = (rows + bm - 1) / bm;
     const long long items = (long long)p.B * (p.H / r.pack) * tiles;
-    // keys of one item, at most
+    // key tiles of one item, at most
     const long long left = p.left < 0 ? kWinUnbounded : p.left, right = p.right < 0 ? kWinUnbounded : p.right;
-    const long long span = std::min((long long)p.Nk, (left + right + 1 + p.sinks) * p.frame + bm);
-    const long long key_tiles = (span + 63) / 64;
-    // four items per SM (one where an item takes a whole SM), shares of at least two key tiles
-    const long long want = (bm == 256 ? 1ll : 4ll) * kPlanSms;
-    const long long splits = std::min(want / items, std::max(1ll, key_tiles / 2));
-    r.splits = (int)std::min<long long>(std::max(1ll, splits), kMaxSplits);
+    const long long span = std::min((long long)p.Nk, (left + right + 1 + p.sinks) * p.frame + std::min(rows, (long long)bm));
+    const long long key_tiles = (span + bn - 1) / bn;
+    // Shares of an item: the count that ends first, at ceil(items * shares / slots) rounds of
+    // ceil(tiles / shares) tiles and a fixed cost of about four 64-key tiles (start, store, join)
+    r.splits = 1;
+    const long long fixed = 256 / bn;
+    long long best = -1;
+    for (int n = 1; n <= kMaxSplits && (n == 1 || n * (128 / bn) <= key_tiles); ++n) {
+        const long long cost = ((items * n + slots - 1) / slots) * ((key_tiles + n - 1) / n + fixed);
+        if (best < 0 || cost < best) {
+            best = cost;
+            r.splits = n;
+        }
+    }
     return r;
 }
 
@@ -330,9 +343,15 @@ scope_status scope_window_attention(const scope_window_params *p, const scope_wi
     a.V = V;
     a.O = O;
     a.lse = lse;
-    if (cudaMemsetAsync(ws, 0, kHeader, s) != cudaSuccess) return SCOPE_ERR_CUDA;
-    const bool tc = a.is_bf16 && (long long)a.pack * a.Nq > 16;
-    cudaError_t e = tc ? window_tc_forward(a, s) : window_simt_forward(a, s);
+    cudaError_t e = cudaSuccess;
+    if (!a.is_bf16) {
+        e = window_simt_forward(a, s);
+    } else if (plan_of(*p).few) {
+        e = window_few_forward(a, s);
+    } else {
+        e = cudaMemsetAsync(ws, 0, kHeader, s);
+        if (e == cudaSuccess) e = window_tc_forward(a, s);
+    }
     if (e == cudaSuccess && a.splits > 1) e = window_join(a, s);
     return cuda_status(e);
 }
@@ -362,9 +381,7 @@ scope_status scope_window_attention_backward(const scope_window_params *p, const
     a.dQ = dQ;
     a.dK = dK;
     a.dV = dV;
-    if (a.is_bf16) return cuda_status(window_tc_backward(a, s));
-    if (cudaMemsetAsync(ws, 0, kHeader, s) != cudaSuccess) return SCOPE_ERR_CUDA;
-    return cuda_status(window_simt_backward(a, s));
+    return cuda_status(a.is_bf16 ? window_tc_backward(a, s) : window_simt_backward(a, s));
 }
 
 }  // extern "C"

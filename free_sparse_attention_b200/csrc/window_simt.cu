@@ -19,21 +19,9 @@ namespace {
 constexpr int kBN = 64;      // columns of a score tile
 constexpr int kLdP = kBN + 4;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-
-template <>
-__device__ __forceinline__ float4 load4<float>(const float *p)
+__device__ __forceinline__ float4 load4(const float *p)
 {
     return *reinterpret_cast<const float4 *>(p);
-}
-
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p)
-{
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ void store4(float *p, float4 v)
@@ -41,24 +29,17 @@ __device__ __forceinline__ void store4(float *p, float4 v)
     *reinterpret_cast<float4 *>(p) = v;
 }
 
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v)
-{
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-}
-
-// Rows of one tile to shared memory as fp32 (leading dimension D + 4); src(r) is row r's
+// Rows of one tile to shared memory (leading dimension D + 4); src(r) is row r's
 // address or NULL for a row of zeros.
-template <typename T, int D, int ROWS, int THREADS, typename Src>
+template <int D, int ROWS, typename Src>
 __device__ __forceinline__ void load_tile(float *dst, Src src)
 {
     constexpr int C4 = D / 4;
 #pragma unroll 4
-    for (int e = threadIdx.x; e < ROWS * C4; e += THREADS) {
+    for (int e = threadIdx.x; e < ROWS * C4; e += 256) {
         const int r = e / C4, c = (e % C4) * 4;
-        const T *p = src(r);
-        store4(dst + r * (D + 4) + c, p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f));
+        const float *p = src(r);
+        store4(dst + r * (D + 4) + c, p ? load4(p + c) : make_float4(0.f, 0.f, 0.f, 0.f));
     }
 }
 
@@ -122,11 +103,13 @@ __device__ __forceinline__ void accumulate(float (&out)[MI][D / 16], const float
 // Forward: BM rows of one unit (b, group of a.pack query heads) against one share of the key
 // tiles they see.  16 x 16 threads (BM = 64, 4 rows each) or 16 x 16 with one row each (BM =
 // 16, the form for few rows, which would leave most of a 64-row tile idle).
-template <typename T, int D, int BM>
+template <int D, int BM>
 __global__ void __launch_bounds__(256) window_fwd_kernel(WinArgs a)
 {
     constexpr int MI = BM / 16;
     extern __shared__ __align__(16) float sm[];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;   // this path has no device conditions
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float *sq = sm, *sk = sq + BM * (D + 4), *sv = sk + kBN * (D + 4), *sp = sv + kBN * (D + 4);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int rows = a.pack * a.Nq, tiles = (rows + BM - 1) / BM;
@@ -146,9 +129,9 @@ __global__ void __launch_bounds__(256) window_fwd_kernel(WinArgs a)
     const WinTiles wt = win_tiles<kBN>(ra, rz);
     const int nt = wt.count(), t0 = (int)((long long)nt * split / a.splits), t1 = (int)((long long)nt * (split + 1) / a.splits);
 
-    load_tile<T, D, BM, 256>(sq, [&](int r) -> const T * {
+    load_tile<D, BM>(sq, [&](int r) -> const float * {
         const int rr = r0 + r;
-        return rr < r1 ? static_cast<const T *>(a.Q) + b * a.lq.b + (h0 + rr / a.Nq) * a.lq.h + (rr % a.Nq) * a.lq.n : nullptr;
+        return rr < r1 ? static_cast<const float *>(a.Q) + b * a.lq.b + (h0 + rr / a.Nq) * a.lq.h + (rr % a.Nq) * a.lq.n : nullptr;
     });
     WinRow lim[MI];
     float m[MI], l[MI], o[MI][D / 16];
@@ -161,15 +144,15 @@ __global__ void __launch_bounds__(256) window_fwd_kernel(WinArgs a)
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) o[i][e] = 0.f;
     }
-    const T *kb = static_cast<const T *>(a.K) + b * a.lk.b + hk * a.lk.h;
-    const T *vb = static_cast<const T *>(a.V) + b * a.lv.b + hk * a.lv.h;
+    const float *kb = static_cast<const float *>(a.K) + b * a.lk.b + hk * a.lk.h;
+    const float *vb = static_cast<const float *>(a.V) + b * a.lv.b + hk * a.lv.h;
     for (int t = t0; t < t1; ++t) {
         const int j0 = wt.at(t) * kBN;
         __syncthreads();
         // keys and values that no row of the tile sees are not read (they may hold anything)
         auto seen = [&](int j) { return j < ra.s || (j >= ra.lo && j < rz.hi); };
-        load_tile<T, D, kBN, 256>(sk, [&](int r) { return seen(j0 + r) ? kb + (j0 + r) * a.lk.n : nullptr; });
-        load_tile<T, D, kBN, 256>(sv, [&](int r) { return seen(j0 + r) ? vb + (j0 + r) * a.lv.n : nullptr; });
+        load_tile<D, kBN>(sk, [&](int r) { return seen(j0 + r) ? kb + (j0 + r) * a.lk.n : nullptr; });
+        load_tile<D, kBN>(sv, [&](int r) { return seen(j0 + r) ? vb + (j0 + r) * a.lv.n : nullptr; });
         __syncthreads();
         float s[MI][4];
         scores<D, MI>(s, sq, sk, ty, tx);
@@ -220,7 +203,7 @@ __global__ void __launch_bounds__(256) window_fwd_kernel(WinArgs a)
                                                            o[i][4 * jj + 3] * inv));
             if (tx == 0) a.part_lse[row * a.splits + split] = lse2;
         } else {
-            T *dst = static_cast<T *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n;
+            float *dst = static_cast<float *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n;
 #pragma unroll
             for (int jj = 0; jj < D / 64; ++jj)
                 store4(dst + 4 * tx + 64 * jj, make_float4(o[i][4 * jj] * inv, o[i][4 * jj + 1] * inv, o[i][4 * jj + 2] * inv,
@@ -236,6 +219,9 @@ template <typename T, int D>
 __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a)
 {
     constexpr int PER = D / 32;
+    // launched while the shares still run (their blocks give the signal); nothing is read before
+    // they are complete
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= (long long)a.B * a.H * a.Nq) return;
@@ -266,11 +252,12 @@ __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a)
 }
 
 // dQ: 64 query rows of one head against the key tiles they see; also writes D_i.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) window_dq_kernel(WinArgs a)
 {
     constexpr int BM = 64, MI = 4;
     extern __shared__ __align__(16) float sm[];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     float *sq = sm, *sg = sq + BM * (D + 4), *sk = sg + BM * (D + 4), *sv = sk + kBN * (D + 4), *sp = sv + kBN * (D + 4);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int tiles = (a.Nq + BM - 1) / BM;
@@ -280,10 +267,10 @@ __global__ void __launch_bounds__(256) window_dq_kernel(WinArgs a)
     const int first = win_first(a, b), kl = win_klen(a, b);
     const WinRow ra = win_row(a, first + r0, kl), rz = win_row(a, first + r1 - 1, kl);
     const WinTiles wt = win_tiles<kBN>(ra, rz);
-    const T *qb = static_cast<const T *>(a.Q) + b * a.lq.b + h * a.lq.h;
-    const T *gb = static_cast<const T *>(a.G) + b * a.lg.b + h * a.lg.h;
-    load_tile<T, D, BM, 256>(sq, [&](int r) { return r0 + r < r1 ? qb + (r0 + r) * a.lq.n : nullptr; });
-    load_tile<T, D, BM, 256>(sg, [&](int r) { return r0 + r < r1 ? gb + (r0 + r) * a.lg.n : nullptr; });
+    const float *qb = static_cast<const float *>(a.Q) + b * a.lq.b + h * a.lq.h;
+    const float *gb = static_cast<const float *>(a.G) + b * a.lg.b + h * a.lg.h;
+    load_tile<D, BM>(sq, [&](int r) { return r0 + r < r1 ? qb + (r0 + r) * a.lq.n : nullptr; });
+    load_tile<D, BM>(sg, [&](int r) { return r0 + r < r1 ? gb + (r0 + r) * a.lg.n : nullptr; });
     __syncthreads();
     WinRow lim[MI];
     float lse[MI], dl[MI], dq[MI][D / 16];
@@ -296,11 +283,11 @@ __global__ void __launch_bounds__(256) window_dq_kernel(WinArgs a)
         lse[i] = in ? a.lse[row] * 1.4426950408889634f : -INFINITY;
         float s = 0.f;
         if (in) {
-            const T *ob = static_cast<const T *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n;
+            const float *ob = static_cast<const float *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n;
 #pragma unroll
             for (int jj = 0; jj < D / 64; ++jj) {
                 const int c = 4 * tx + 64 * jj;
-                dot4(s, load4<T>(ob + c), *reinterpret_cast<const float4 *>(sg + (ty + 16 * i) * (D + 4) + c));
+                dot4(s, load4(ob + c), *reinterpret_cast<const float4 *>(sg + (ty + 16 * i) * (D + 4) + c));
             }
         }
 #pragma unroll
@@ -310,14 +297,14 @@ __global__ void __launch_bounds__(256) window_dq_kernel(WinArgs a)
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) dq[i][e] = 0.f;
     }
-    const T *kb = static_cast<const T *>(a.K) + b * a.lk.b + hk * a.lk.h;
-    const T *vb = static_cast<const T *>(a.V) + b * a.lv.b + hk * a.lv.h;
+    const float *kb = static_cast<const float *>(a.K) + b * a.lk.b + hk * a.lk.h;
+    const float *vb = static_cast<const float *>(a.V) + b * a.lv.b + hk * a.lv.h;
     for (int t = 0; t < wt.count(); ++t) {
         const int j0 = wt.at(t) * kBN;
         __syncthreads();
         auto seen = [&](int j) { return j < ra.s || (j >= ra.lo && j < rz.hi); };
-        load_tile<T, D, kBN, 256>(sk, [&](int r) { return seen(j0 + r) ? kb + (j0 + r) * a.lk.n : nullptr; });
-        load_tile<T, D, kBN, 256>(sv, [&](int r) { return seen(j0 + r) ? vb + (j0 + r) * a.lv.n : nullptr; });
+        load_tile<D, kBN>(sk, [&](int r) { return seen(j0 + r) ? kb + (j0 + r) * a.lk.n : nullptr; });
+        load_tile<D, kBN>(sv, [&](int r) { return seen(j0 + r) ? vb + (j0 + r) * a.lv.n : nullptr; });
         __syncthreads();
         float s[MI][4], dp[MI][4];
         scores<D, MI>(s, sq, sk, ty, tx);
@@ -334,7 +321,7 @@ __global__ void __launch_bounds__(256) window_dq_kernel(WinArgs a)
         __syncwarp();
         accumulate<D, MI>(dq, sp, sk, ty, tx);
     }
-    T *dst = static_cast<T *>(a.dQ) + b * a.ldq.b + h * a.ldq.h;
+    float *dst = static_cast<float *>(a.dQ) + b * a.ldq.b + h * a.ldq.h;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         const int q = r0 + ty + 16 * i;
@@ -349,7 +336,7 @@ __global__ void __launch_bounds__(256) window_dq_kernel(WinArgs a)
 
 // dK, dV: 64 keys of one key head against every query (of all its query heads, in order) that
 // may see one of them.  Scores are taken transposed: rows are keys, columns are queries.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) window_dkv_kernel(WinArgs a)
 {
     constexpr int BM = 64, MI = 4;
@@ -364,10 +351,10 @@ __global__ void __launch_bounds__(256) window_dkv_kernel(WinArgs a)
     const int j0 = tile * BM, j1 = min(a.Nk, j0 + BM);
     const int first = win_first(a, b), kl = win_klen(a, b);
     const int2 qr = win_queries(a, first, kl, a.Nq, j0, j1);
-    const T *kb = static_cast<const T *>(a.K) + b * a.lk.b + hk * a.lk.h;
-    const T *vb = static_cast<const T *>(a.V) + b * a.lv.b + hk * a.lv.h;
-    load_tile<T, D, BM, 256>(sk, [&](int r) { return j0 + r < min(j1, kl) ? kb + (j0 + r) * a.lk.n : nullptr; });
-    load_tile<T, D, BM, 256>(sv, [&](int r) { return j0 + r < min(j1, kl) ? vb + (j0 + r) * a.lv.n : nullptr; });
+    const float *kb = static_cast<const float *>(a.K) + b * a.lk.b + hk * a.lk.h;
+    const float *vb = static_cast<const float *>(a.V) + b * a.lv.b + hk * a.lv.h;
+    load_tile<D, BM>(sk, [&](int r) { return j0 + r < min(j1, kl) ? kb + (j0 + r) * a.lk.n : nullptr; });
+    load_tile<D, BM>(sv, [&](int r) { return j0 + r < min(j1, kl) ? vb + (j0 + r) * a.lv.n : nullptr; });
     float dk[MI][D / 16], dv[MI][D / 16];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -375,12 +362,12 @@ __global__ void __launch_bounds__(256) window_dkv_kernel(WinArgs a)
         for (int e = 0; e < D / 16; ++e) dk[i][e] = dv[i][e] = 0.f;
     for (int g = 0; g < G; ++g) {
         const int h = hk * G + g;
-        const T *qb = static_cast<const T *>(a.Q) + b * a.lq.b + h * a.lq.h;
-        const T *gb = static_cast<const T *>(a.G) + b * a.lg.b + h * a.lg.h;
+        const float *qb = static_cast<const float *>(a.Q) + b * a.lq.b + h * a.lq.h;
+        const float *gb = static_cast<const float *>(a.G) + b * a.lg.b + h * a.lg.h;
         for (int i0 = qr.x; i0 < qr.y; i0 += kBN) {
             __syncthreads();
-            load_tile<T, D, kBN, 256>(sq, [&](int r) { return i0 + r < qr.y ? qb + (i0 + r) * a.lq.n : nullptr; });
-            load_tile<T, D, kBN, 256>(sg, [&](int r) { return i0 + r < qr.y ? gb + (i0 + r) * a.lg.n : nullptr; });
+            load_tile<D, kBN>(sq, [&](int r) { return i0 + r < qr.y ? qb + (i0 + r) * a.lq.n : nullptr; });
+            load_tile<D, kBN>(sg, [&](int r) { return i0 + r < qr.y ? gb + (i0 + r) * a.lg.n : nullptr; });
             __syncthreads();
             float s[MI][4], dp[MI][4];
             scores<D, MI>(s, sk, sq, ty, tx);
@@ -406,7 +393,7 @@ __global__ void __launch_bounds__(256) window_dkv_kernel(WinArgs a)
             accumulate<D, MI>(dk, sd, sq, ty, tx);
         }
     }
-    T *dkb = static_cast<T *>(a.dK) + b * a.ldk.b + hk * a.ldk.h, *dvb = static_cast<T *>(a.dV) + b * a.ldv.b + hk * a.ldv.h;
+    float *dkb = static_cast<float *>(a.dK) + b * a.ldk.b + hk * a.ldk.h, *dvb = static_cast<float *>(a.dV) + b * a.ldv.b + hk * a.ldv.h;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         const int j = j0 + ty + 16 * i;
@@ -431,24 +418,24 @@ cudaError_t launch(F *kernel, long long grid, int smem, const WinArgs &a, cudaSt
     return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t forward(const WinArgs &a, cudaStream_t s)
 {
     // 16-row tiles when a unit's rows fill at most one of them, 64-row tiles otherwise
     const long long rows = (long long)a.pack * a.Nq, units = (long long)a.B * (a.H / a.pack);
     if (rows <= 16)
-        return launch(window_fwd_kernel<T, D, 16>, units * a.splits, (16 + 2 * kBN) * (D + 4) * 4 + 16 * kLdP * 4, a, s);
-    return launch(window_fwd_kernel<T, D, 64>, units * ((rows + 63) / 64) * a.splits,
+        return launch(window_fwd_kernel<D, 16>, units * a.splits, (16 + 2 * kBN) * (D + 4) * 4 + 16 * kLdP * 4, a, s);
+    return launch(window_fwd_kernel<D, 64>, units * ((rows + 63) / 64) * a.splits,
                   (64 + 2 * kBN) * (D + 4) * 4 + 64 * kLdP * 4, a, s);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t backward(const WinArgs &a, cudaStream_t s)
 {
-    cudaError_t e = launch(window_dq_kernel<T, D>, (long long)a.B * a.H * ((a.Nq + 63) / 64),
+    cudaError_t e = launch(window_dq_kernel<D>, (long long)a.B * a.H * ((a.Nq + 63) / 64),
                            4 * 64 * (D + 4) * 4 + 64 * kLdP * 4, a, s);
     if (e != cudaSuccess) return e;
-    return launch(window_dkv_kernel<T, D>, (long long)a.B * a.Hkv * ((a.Nk + 63) / 64),
+    return launch(window_dkv_kernel<D>, (long long)a.B * a.Hkv * ((a.Nk + 63) / 64),
                   4 * 64 * (D + 4) * 4 + 2 * 64 * kLdP * 4, a, s);
 }
 
@@ -456,28 +443,31 @@ cudaError_t backward(const WinArgs &a, cudaStream_t s)
 
 cudaError_t window_simt_forward(const WinArgs &a, cudaStream_t s)
 {
-    if (a.is_bf16) return a.d == 64 ? forward<__nv_bfloat16, 64>(a, s) : forward<__nv_bfloat16, 128>(a, s);
-    return a.d == 64 ? forward<float, 64>(a, s) : forward<float, 128>(a, s);
+    return a.d == 64 ? forward<64>(a, s) : forward<128>(a, s);
 }
 
 cudaError_t window_simt_backward(const WinArgs &a, cudaStream_t s)
 {
-    if (a.is_bf16) return a.d == 64 ? backward<__nv_bfloat16, 64>(a, s) : backward<__nv_bfloat16, 128>(a, s);
-    return a.d == 64 ? backward<float, 64>(a, s) : backward<float, 128>(a, s);
+    return a.d == 64 ? backward<64>(a, s) : backward<128>(a, s);
 }
 
 cudaError_t window_join(const WinArgs &a, cudaStream_t s)
 {
     const long long rows = (long long)a.B * a.H * a.Nq;
-    const unsigned grid = (unsigned)((rows + 3) / 4);
-    if (a.is_bf16) {
-        if (a.d == 64) window_join_kernel<__nv_bfloat16, 64><<<grid, 128, 0, s>>>(a);
-        else window_join_kernel<__nv_bfloat16, 128><<<grid, 128, 0, s>>>(a);
-    } else {
-        if (a.d == 64) window_join_kernel<float, 64><<<grid, 128, 0, s>>>(a);
-        else window_join_kernel<float, 128><<<grid, 128, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)((rows + 3) / 4));
+    c.blockDim = dim3(128);
+    c.stream = s;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    if (a.is_bf16)
+        return a.d == 64 ? cudaLaunchKernelEx(&c, window_join_kernel<__nv_bfloat16, 64>, a)
+                         : cudaLaunchKernelEx(&c, window_join_kernel<__nv_bfloat16, 128>, a);
+    return a.d == 64 ? cudaLaunchKernelEx(&c, window_join_kernel<float, 64>, a)
+                     : cudaLaunchKernelEx(&c, window_join_kernel<float, 128>, a);
 }
 
 }  // namespace scope

@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return it;
     };
     if (warp == 8 && lane == 0) fetch(0);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
