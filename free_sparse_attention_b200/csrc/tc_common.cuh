@@ -96,15 +96,29 @@ struct Waiter {
     unsigned long long limit_ns;
 };
 
-// Bounded wait by one thread (as bar_wait, with the launch's limit).
+// Test of an mbarrier phase that suspends the thread until the phase completes, for kTryNs at
+// most: a completed phase wakes it at once, and it takes no issue slots meanwhile.
+constexpr uint32_t kTryNs = 10000;
+__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity), "r"(kTryNs)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait by one thread (as bar_wait, with the launch's limit).  The abort flag and the
+// timer, whose read takes hundreds of cycles, are looked at between suspended tests only.
 __device__ __forceinline__ bool wait1(uint64_t *b, uint32_t parity, const Waiter &w)
 {
-    if (bar_test(b, parity)) return true;
+    if (bar_try(b, parity)) return true;
     const unsigned long long t0 = global_ns();
-    unsigned ns = 8;
-    while (!bar_test(b, parity)) {
-        __nanosleep(ns);
-        ns = ns < 64 ? ns * 2 : 64;
+    while (!bar_try(b, parity)) {
         if (*w.abort_flag) return false;
         if (global_ns() - t0 > w.limit_ns) {
             *w.abort_flag = 1;
@@ -115,14 +129,16 @@ __device__ __forceinline__ bool wait1(uint64_t *b, uint32_t parity, const Waiter
     return true;
 }
 
-// Warp-uniform wait: lane 0 polls, every lane gets the same answer.
+// Warp-uniform wait: every lane tests (one instruction for the warp), and a vote makes the
+// answer the same for all; the waiting itself is lane 0's.
 __device__ __forceinline__ bool waitw(uint64_t *b, uint32_t parity, const Waiter &w)
 {
+    if (__all_sync(0xffffffffu, bar_test(b, parity))) return true;
     int ok = 0;
     if ((threadIdx.x & 31) == 0) ok = wait1(b, parity, w) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
-    return ok != 0;
+    // the other lanes acquire the phase that lane 0 saw complete
+    return __all_sync(0xffffffffu, ok != 0 && bar_test(b, parity));
 }
 
 // A wait with no abort check, for draining work already issued (bounded all the same).

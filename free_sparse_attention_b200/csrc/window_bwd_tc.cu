@@ -9,12 +9,17 @@
 //            rows R1, R2   columns C1, C2   S = R1 C1^T  dP = R2 C2^T   results
 //   dQ       Q, dO         K, V             S            dP             dQ += dS C1
 //   dK, dV   K, V          Q, dO            S^T          dP^T           dK += dS C1, dV += P C2
-// Per CTA (persistent, one per SM): warps 0-3 / 4-7 turn S and dP of even / odd steps into P and
-// dS (thread r owns row r = TMEM lane r); warp 8 loads rows and column tiles by TMA and hands out
-// the items; warp 9 stages lse and D of the columns (dK, dV); warp 10 issues S and dP of a step
-// (two buffers, so it runs up to two steps ahead); warp 11 issues the products of P and dS, read
-// from TMEM where they replace S and dP.  P and dS are rounded to bf16 once, as operands;
-// everything summed is fp32.
+// Per CTA (persistent, one per SM): warps 0-15 turn S and dP into P and dS, two warpgroups (thread
+// r of each owns row r = TMEM lane r, one 32 of the columns) for even and two for odd steps; warp 16
+// loads rows and column tiles by TMA and hands out the items; warp 17 stages lse and D of the
+// columns (dK, dV); warp 18 issues S and dP; warp 19 issues the products of P and dS, read as
+// operands from TMEM.
+// What bounds a step is the chain product -> commit -> wait -> arithmetic -> arrive -> product
+// (about 3500 cycles when one buffer goes through all of it), so the chain is cut where TMEM has
+// room: S and dP are released as soon as they are in registers, P and dS have columns of their
+// own, and every operand has its own barrier (dV starts on P while dS is computed).  Only dK, dV
+// at d = 128 has no such room (2 x 128 columns of results): there P and dS replace S and dP.
+// P and dS are rounded to bf16 once, as operands; everything summed is fp32.
 #include "window_tc.cuh"
 
 namespace scope {
@@ -22,30 +27,53 @@ namespace scope {
 namespace {
 
 constexpr int kBM = 128, kBN = 64;
-constexpr int kWarps = 12, kThreads = kWarps * 32;
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
-static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "register split");
-constexpr int kMaxStages = 6, kRing = 4;
+constexpr int kWarps = 20, kThreads = kWarps * 32;
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;   // 65536 / 640, a multiple of 8
+static_assert(4 * kSoftmaxRegs + kOtherRegs == 5 * kLaunchRegs, "register split");
+constexpr int kMaxStages = 8, kMaxBuf = 3, kRing = 4;
 constexpr uint32_t kTmemCols = 512;
 
 struct __align__(8) Bars {
     uint64_t r_full, r_empty, land, out_full, out_free;
     uint64_t c_full[kMaxStages], c_empty[kMaxStages], ls_full[kMaxStages];
-    uint64_t s_full[2], p_full[2], buf_free[2], drain[2];
+    uint64_t s_full[kMaxBuf], d_full[kMaxBuf], s_free[kMaxBuf], d_free[kMaxBuf];   // S and dP buffers
+    uint64_t p_full[2], ds_full[2], pd_free[2], drain[2];                          // P and dS buffers
     uint64_t item_full[kRing], item_empty[kRing];
 };
 
-template <int D>
+// TMEM columns: kBuf buffers of S (64) and dP (64); then, unless they share those, two buffers
+// of P (dK, dV only) and dS (32 each); then the results (D each).
+template <bool DKV, int D>
+struct Cols {
+    static constexpr bool kShared = DKV && D == 128;   // P and dS replace S and dP
+    static constexpr int kBuf = !DKV && D == 64 ? 3 : 2;
+    static constexpr int kPd = kBuf * 128;
+    static constexpr int kPdBuf = kShared ? 0 : (DKV ? 64 : 32);
+    static constexpr int kOut = kPd + 2 * kPdBuf;
+    static_assert(kOut + (DKV ? 2 : 1) * D <= (int)kTmemCols, "TMEM columns");
+    // column of the bf16 pairs of columns 16 kk .. 16 kk + 15 of P / dS of step g
+    static __device__ __forceinline__ uint32_t p(uint32_t g, int kk)
+    {
+        return kShared ? (g % 2) * 128 + (kk >> 1) * 32 + (kk & 1) * 8 : kPd + (g & 1) * kPdBuf + kk * 8;
+    }
+    static __device__ __forceinline__ uint32_t ds(uint32_t g, int kk)
+    {
+        return kShared ? p(g, kk) + 64 : kPd + (g & 1) * kPdBuf + (DKV ? 32 : 0) + kk * 8;
+    }
+};
+
+template <bool DKV, int D>
 struct Smem {
-    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kStages = D == 128 ? (DKV ? 4 : 5) : 8;
     static constexpr int kRows = kBM * D * 2, kTile = kBN * D * 2;
     static constexpr int kR1 = 0, kR2 = kRows, kC = 2 * kRows;               // stage s: C1, C2
     static constexpr int kLs = kC + kStages * 2 * kTile;                     // stage s: lse [64], D [64]
-    static constexpr int kBars = kLs + kStages * 2 * kBN * 4;
+    static constexpr int kBars = kLs + (DKV ? kStages * 2 * kBN * 4 : 0);
     static constexpr int kMisc = kBars + (int)sizeof(Bars);
     static constexpr int kAlloc = kMisc + 64 + 1024;
     static_assert(kAlloc <= 232448, "shared memory budget");
     static_assert(kAlloc > 232448 / 2, "one CTA (and its 512 TMEM columns) per SM");
+    static_assert(kStages <= kMaxStages, "ring depth");
 };
 
 // One item: 128 rows of one head, and its column tiles in order.
@@ -114,8 +142,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tmC1, const __grid_constant__ CUtensorMap tmC2,
                          const __grid_constant__ WinArgs a, int n_items)
 {
-    using L = Smem<D>;
-    constexpr int NB = D / 64, NS = L::kStages;
+    using L = Smem<DKV, D>;
+    using T = Cols<DKV, D>;
+    constexpr int NB = D / 64, NS = L::kStages, NBUF = T::kBuf;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars *bars = reinterpret_cast<Bars *>(sm + L::kBars);
@@ -134,16 +163,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&bars->r_empty, 1);
         bar_init(&bars->land, 1);
         bar_init(&bars->out_full, 1);
-        bar_init(&bars->out_free, 8);
+        bar_init(&bars->out_free, 16);
         for (int s = 0; s < kMaxStages; ++s) {
             bar_init(&bars->c_full[s], 1);
             bar_init(&bars->c_empty[s], 1);
             bar_init(&bars->ls_full[s], 1);
         }
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < kMaxBuf; ++w) {
             bar_init(&bars->s_full[w], 1);
-            bar_init(&bars->p_full[w], 4);
-            bar_init(&bars->buf_free[w], 1);
+            bar_init(&bars->d_full[w], 1);
+            bar_init(&bars->s_free[w], T::kShared ? 1 : 8);   // the product's commit, or the 8 warps
+            bar_init(&bars->d_free[w], T::kShared ? 1 : 8);
+        }
+        for (int w = 0; w < 2; ++w) {
+            bar_init(&bars->p_full[w], 8);
+            bar_init(&bars->ds_full[w], 8);
+            bar_init(&bars->pd_free[w], 1);
             bar_init(&bars->drain[w], 1);
         }
         for (int k = 0; k < kRing; ++k) {
@@ -152,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 10) {
+    if (warp == 18) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");
@@ -162,10 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // TMEM columns: buffer w: S at 128 w, dP at 128 w + 64 (P, dS as bf16 pairs over the first 32
-    // of each); out1 (dQ or dK) at 256, out2 (dV) at 256 + D
-    const uint32_t out1 = tmem + 256, out2 = tmem + 256 + D;
-    auto fetch = [&](uint32_t k) -> bool {   // lane 0 of warp 8: the item scheduler
+    const uint32_t out1 = tmem + T::kOut, out2 = out1 + D;   // dQ or dK; dV
+    auto fetch = [&](uint32_t k) -> bool {   // lane 0 of warp 16: the item scheduler
         const int slot = k % kRing;
         if (!wait1(&bars->item_empty[slot], ((k / kRing) & 1) ^ 1, W)) return false;
         const int it = atomicAdd(counter, 1);
@@ -179,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int it = ring[slot];
         __syncwarp();
         if (lane == 0) bar_arrive(&bars->item_empty[slot]);
-        if (warp == 8 && it >= 0) {
+        if (warp == 16 && it >= 0) {
             int ok = 1;
             if (lane == 0) ok = fetch(k + 1) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -187,14 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return it;
     };
-    if (warp == 8 && lane == 0) fetch(0);
+    if (warp == 16 && lane == 0) fetch(0);
 
-    // Every role counts the CTA's steps in g: step g uses buffer g % 2 (use g / 2) and column
-    // stage g % NS (use g / NS).
+    // Every role counts the CTA's steps in g: step g uses S / dP buffer g % NBUF, P / dS buffer
+    // g % 2 and column stage g % NS; phase parities follow from the quotients.
     uint32_t g = 0;
-    if (warp >= 8) {
+    if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8) {
+        if (warp == 16) {
             // ------------------------------------------------------------------ loads
             uint32_t r_it = 0, land = 0;
             bool landing = false;
@@ -268,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (r_it > 0) drain_wait(&bars->r_full, (r_it - 1) & 1, W.limit_ns);
             }
             __syncwarp();
-        } else if (warp == 9) {
+        } else if (warp == 17) {
             // ------------------------------------------------------------------ lse and D of the columns
             for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
                 const int it = next_item(item_k);
@@ -306,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (lane == 0) {
             // ------------------------------------------------------------------ product issuers
             constexpr uint32_t idesc_s = f16_idesc(kBM, kBN, false), idesc_o = f16_idesc(kBM, D, true);
-            const bool first_products = warp == 10;
+            const bool first_products = warp == 18;
             const uint64_t r1 = sw128_desc(sbase + L::kR1, 16, 1024), r2 = sw128_desc(sbase + L::kR2, 16, 1024);
             uint32_t items = 0;
             bool issued = false;
@@ -323,8 +356,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (first_products) {
                     ok = wait1(&bars->r_full, items & 1, W);
                     for (int t = 0; t < steps && ok; ++t, ++g) {
-                        const int s = g % NS, w = g & 1;
-                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W) && wait1(&bars->buf_free[w], ((g >> 1) & 1) ^ 1, W);
+                        const int s = g % NS, w = g % NBUF;
+                        const uint32_t use = ((g / NBUF) & 1) ^ 1;
+                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W) && wait1(&bars->s_free[w], use, W);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t cb = sbase + L::kC + s * 2 * L::kTile;
@@ -335,35 +369,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
                             mma_bf16(tmem + 128 * w, r1 + offa, c1 + offb, idesc_s, kk > 0);
                         }
+                        mma_commit(&bars->s_full[w]);
+                        ok = wait1(&bars->d_free[w], use, W);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t offa = (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
                             const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
                             mma_bf16(tmem + 128 * w + 64, r2 + offa, c2 + offb, idesc_s, kk > 0);
                         }
-                        mma_commit(&bars->s_full[w]);
+                        mma_commit(&bars->d_full[w]);
                         if (t == steps - 1) mma_commit(&bars->r_empty);
                     }
                 } else {
                     for (int t = 0; t < steps && ok; ++t, ++g) {
                         const int s = g % NS, w = g & 1;
-                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W) && wait1(&bars->p_full[w], (g >> 1) & 1, W);
+                        const uint32_t use = (g >> 1) & 1;
+                        const uint32_t cb = sbase + L::kC + s * 2 * L::kTile;
+                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W);
                         if (ok && t == 0) ok = wait1(&bars->out_free, (items & 1) ^ 1, W);
                         if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t cb = sbase + L::kC + s * 2 * L::kTile;
-                        const uint64_t c1 = sw128_desc(cb, kBN * 128, 1024), c2 = sw128_desc(cb + L::kTile, kBN * 128, 1024);
                         if constexpr (DKV) {
+                            const uint64_t c2 = sw128_desc(cb + L::kTile, kBN * 128, 1024);
+                            ok = wait1(&bars->p_full[w], use, W);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll
                             for (int kk = 0; kk < kBN / 16; ++kk)
-                                mma_bf16_ts(out2, tmem + 128 * w + kk * 8, c2 + (uint64_t)(kk * 2048 >> 4), idesc_o,
+                                mma_bf16_ts(out2, tmem + T::p(g, kk), c2 + (uint64_t)(kk * 2048 >> 4), idesc_o,
                                             (t > 0 || kk > 0) ? 1u : 0u);
+                            if constexpr (T::kShared) mma_commit(&bars->s_free[w]);
                         }
+                        const uint64_t c1 = sw128_desc(cb, kBN * 128, 1024);
+                        ok = wait1(&bars->ds_full[w], use, W);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
-                            mma_bf16_ts(out1, tmem + 128 * w + 64 + kk * 8, c1 + (uint64_t)(kk * 2048 >> 4), idesc_o,
+                            mma_bf16_ts(out1, tmem + T::ds(g, kk), c1 + (uint64_t)(kk * 2048 >> 4), idesc_o,
                                         (t > 0 || kk > 0) ? 1u : 0u);
-                        mma_commit(&bars->buf_free[w]);
+                        mma_commit(T::kShared ? &bars->d_free[w] : &bars->pd_free[w]);
                         mma_commit(&bars->c_empty[s]);
                         if (t == steps - 1) mma_commit(&bars->out_full);
                     }
@@ -372,15 +418,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++items;
             }
             if (issued) {   // every product issued completes before TMEM is freed
-                mma_commit(&bars->drain[warp - 10]);
-                drain_wait(&bars->drain[warp - 10], 0, W.limit_ns);
+                mma_commit(&bars->drain[warp - 18]);
+                drain_wait(&bars->drain[warp - 18], 0, W.limit_ns);
             }
         }
         __syncwarp();
     } else {
         // ---------------------------------------------------------------------- P and dS, epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        const int wg = warp >> 2, row = threadIdx.x - wg * kBM;
+        // warpgroup: column half, and the parity of its steps (two steps in work at a time hide the
+        // latencies of each other's barriers and TMEM accesses)
+        const int wg = (warp >> 2) & 1, odd = warp >> 3, row = threadIdx.x & (kBM - 1);
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         uint32_t items = 0;
         for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
@@ -406,100 +454,137 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned long long c2 = f2pack(a.scale_log2, a.scale_log2);
             bool ok = true;
             for (int t = 0; t < x.steps; ++t, ++g) {
-                if ((int)(g & 1) != wg) continue;
-                const int s = g % NS;
-                const int j0 = column_of<DKV>(a, x, t).y;
+                if ((int)(g & 1) != odd) continue;
+                const int s = g % NS, w = g % NBUF, j0 = column_of<DKV>(a, x, t).y + 32 * wg;
+                const uint32_t use = (g / NBUF) & 1;
+                const uint32_t sb = tmem + lane_base + 128 * w + 32 * wg;   // this warpgroup's 32 columns of S
+                auto below = [&](int e) { return e <= 0 ? 0u : (e >= 32 ? ~0u : (1u << e) - 1u); };
+                const uint32_t vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
+                const bool whole = __all_sync(0xffffffffu, vis == ~0u);
                 if constexpr (DKV) ok = waitw(&bars->ls_full[s], (g / NS) & 1, W);
-                ok = ok && waitw(&bars->s_full[wg], (g >> 1) & 1, W);
+                ok = ok && waitw(&bars->s_full[w], use, W);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t sb = tmem + lane_base + 128 * wg;
-                float sv[kBN], dv[kBN];
-                tmem_ld32(sb, sv);
-                tmem_ld32(sb + 64, dv);
-                tmem_ld32(sb + 32, sv + 32);
-                tmem_ld32(sb + 96, dv + 32);
-                auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
-                const unsigned long long vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
-                const bool whole = __all_sync(0xffffffffu, vis == ~0ull);
+                float v[32];
+                tmem_ld32(sb, v);
                 tmem_wait_ld();
-                const float *ls = reinterpret_cast<const float *>(sm + L::kLs) + s * 2 * kBN;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pp[16], pd[16];
-                    const uint32_t bits = (uint32_t)(vis >> (32 * h));
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float4 l4, d4;
-                        if constexpr (DKV) {
-                            l4 = *reinterpret_cast<const float4 *>(ls + 32 * h + 2 * e);
-                            d4 = *reinterpret_cast<const float4 *>(ls + kBN + 32 * h + 2 * e);
-                        } else {
-                            l4 = make_float4(nlse, nlse, nlse, nlse);
-                            d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int j = 32 * h + 2 * (e + k);
-                            const float2 ex = f2unpack(f2fma(f2pack(sv[j], sv[j + 1]), c2,
-                                                             k ? f2pack(l4.z, l4.w) : f2pack(l4.x, l4.y)));
-                            float p0 = fast_exp2(ex.x), p1 = fast_exp2(ex.y);
-                            const float2 dd = f2unpack(f2add(f2pack(dv[j], dv[j + 1]),
-                                                             k ? f2pack(d4.z, d4.w) : f2pack(d4.x, d4.y)));
-                            float s0 = p0 * dd.x, s1 = p1 * dd.y;
-                            if (!whole) {
-                                const bool v0 = (bits >> (2 * (e + k))) & 1u, v1 = (bits >> (2 * (e + k) + 1)) & 1u;
-                                p0 = v0 ? p0 : 0.f;
-                                p1 = v1 ? p1 : 0.f;
-                                s0 = v0 ? s0 : 0.f;
-                                s1 = v1 ? s1 : 0.f;
-                            }
-                            __nv_bfloat162 q2 = __floats2bfloat162_rn(p0, p1), d2 = __floats2bfloat162_rn(s0, s1);
-                            pp[e + k] = *reinterpret_cast<uint32_t *>(&q2);
-                            pd[e + k] = *reinterpret_cast<uint32_t *>(&d2);
-                        }
-                    }
-                    if constexpr (DKV) tmem_st16(sb + h * 16, pp);
-                    tmem_st16(sb + 64 + h * 16, pd);
+                if constexpr (!T::kShared) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&bars->s_free[w]);
                 }
+                // P of the columns the row sees, 0 elsewhere
+                const float *ls = reinterpret_cast<const float *>(sm + L::kLs) + s * 2 * kBN + 32 * wg;
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 l4 = make_float4(nlse, nlse, nlse, nlse);
+                    if constexpr (DKV) l4 = *reinterpret_cast<const float4 *>(ls + e);
+                    const float2 x0 = f2unpack(f2fma(f2pack(v[e], v[e + 1]), c2, f2pack(l4.x, l4.y)));
+                    const float2 x1 = f2unpack(f2fma(f2pack(v[e + 2], v[e + 3]), c2, f2pack(l4.z, l4.w)));
+                    v[e] = fast_exp2(x0.x);
+                    v[e + 1] = fast_exp2(x0.y);
+                    v[e + 2] = fast_exp2(x1.x);
+                    v[e + 3] = fast_exp2(x1.y);
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0.f;
+                }
+                if constexpr (DKV) {
+                    // the shared buffers: this half's 16 columns lie under its own 32 of S
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                        pk[e] = *reinterpret_cast<uint32_t *>(&h2);
+                    }
+                    if constexpr (!T::kShared) {
+                        ok = waitw(&bars->pd_free[g & 1], ((g >> 1) & 1) ^ 1, W);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    tmem_st16(tmem + lane_base + T::p(g, 2 * wg), pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&bars->p_full[g & 1]);
+                }
+                ok = waitw(&bars->d_full[w], use, W);
+                if (!ok) break;
+                tc_fence_after();
+                float dv[32];
+                tmem_ld32(sb + 64, dv);
+                tmem_wait_ld();
+                if constexpr (!T::kShared) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&bars->d_free[w]);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
+                    if constexpr (DKV) d4 = *reinterpret_cast<const float4 *>(ls + kBN + e);
+                    const float2 x0 = f2unpack(f2add(f2pack(dv[e], dv[e + 1]), f2pack(d4.x, d4.y)));
+                    const float2 x1 = f2unpack(f2add(f2pack(dv[e + 2], dv[e + 3]), f2pack(d4.z, d4.w)));
+                    v[e] *= x0.x;
+                    v[e + 1] *= x0.y;
+                    v[e + 2] *= x1.x;
+                    v[e + 3] *= x1.y;
+                }
+                if (!whole) {   // 0 x what a hidden column holds
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                    pk[e] = *reinterpret_cast<uint32_t *>(&h2);
+                }
+                if constexpr (!DKV) {
+                    ok = waitw(&bars->pd_free[g & 1], ((g >> 1) & 1) ^ 1, W);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                tmem_st16(tmem + lane_base + T::ds(g, 2 * wg), pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bars->p_full[wg]);
+                if (lane == 0) bar_arrive(&bars->ds_full[g & 1]);
             }
             if (!ok) break;
-            // epilogue: dK by warpgroup 0 and dV by 1; of dQ, half the channels each
+            // epilogue: of dK and dV half the channels each, of dQ a quarter
             if (x.steps > 0) {
                 if (!waitw(&bars->out_full, items & 1, W)) break;
                 ++items;
                 tc_fence_after();
             }
-            constexpr int CH = DKV ? D : D / 2;   // channels of one warpgroup
-            const uint32_t src = tmem + lane_base + (DKV ? 256 + wg * D : 256 + wg * CH);
+            constexpr int CH = DKV ? D / 2 : D / 4;   // channels of one warpgroup
+            const int ch0 = DKV ? odd * CH : (2 * wg + odd) * CH;
+            const uint32_t src = (DKV && wg == 1 ? out2 : out1) + lane_base + ch0;
             const float scale = DKV && wg == 1 ? 1.f : a.scale;
             const WinLayout lay = DKV ? (wg ? a.ldv : a.ldk) : a.ldq;
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(DKV ? (wg ? a.dV : a.dK) : a.dQ) + x.b * lay.b + x.h * lay.h +
-                                 (x.r0 + row) * lay.n + (DKV ? 0 : wg * CH);
+                                 (x.r0 + row) * lay.n + ch0;
 #pragma unroll 1
-            for (int h = 0; h < CH / 32; ++h) {
-                float o[32];
+            for (int h = 0; h < CH / 16; ++h) {
+                float o[16];
                 if (x.steps > 0) {
-                    tmem_ld32(src + h * 32, o);
+                    tmem_ld16(src + h * 16, o);
                     tmem_wait_ld();
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    for (int e = 0; e < 16; ++e) o[e] = 0.f;
                 }
                 if (!valid) continue;
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
+                for (int e = 0; e < 16; e += 8) {
                     uint32_t pk[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         __nv_bfloat162 hh = __floats2bfloat162_rn(o[e + 2 * k] * scale, o[e + 2 * k + 1] * scale);
                         pk[k] = *reinterpret_cast<uint32_t *>(&hh);
                     }
-                    *reinterpret_cast<uint4 *>(dst + h * 32 + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    *reinterpret_cast<uint4 *>(dst + h * 16 + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
             }
             if (x.steps > 0) {
@@ -512,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 10)
+    if (warp == 18)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
@@ -561,7 +646,7 @@ cudaError_t launch_pass(const WinArgs &a, cudaStream_t s)
         return cudaErrorInvalidDeviceFunction;
     const long long items = DKV ? (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM) : (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM);
     if (items > 0x7ffffff0ll) return cudaErrorInvalidConfiguration;
-    const int smem = Smem<D>::kAlloc;
+    const int smem = Smem<DKV, D>::kAlloc;
     cudaError_t e = cudaFuncSetAttribute(window_bwd_tc_kernel<DKV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     window_bwd_tc_kernel<DKV, D><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(r1, r2, c1, c2, a,
