@@ -11,9 +11,9 @@
 //   dK, dV   K, V          Q, dO            S^T          dP^T           dK += dS C1, dV += P C2
 // Per CTA (persistent, one per SM): warps 0-15 turn S and dP into P and dS, two warpgroups (thread
 // r of each owns row r = TMEM lane r, one 32 of the columns) for even and two for odd steps; warp 16
-// loads rows and column tiles by TMA and hands out the items; warp 17 stages lse and D of the
-// columns (dK, dV); warp 18 issues S and dP; warp 19 issues the products of P and dS, read as
-// operands from TMEM.
+// loads rows and column tiles by TMA (and lse and D of the columns, for dK, dV) and hands out the
+// items; warps 18 and 17 issue S and dP, warp 19 the products of P and dS, read as operands from
+// TMEM.
 // What bounds a step is the chain product -> commit -> wait -> arithmetic -> arrive -> product
 // (about 3500 cycles when one buffer goes through all of it), so the chain is cut where TMEM has
 // room: S and dP are released as soon as they are in registers, P and dS have columns of their
@@ -37,7 +37,7 @@ struct __align__(8) Bars {
     uint64_t r_full, r_empty, land, out_full, out_free;
     uint64_t c_full[kMaxStages], c_empty[kMaxStages], ls_full[kMaxStages];
     uint64_t s_full[kMaxBuf], d_full[kMaxBuf], s_free[kMaxBuf], d_free[kMaxBuf];   // S and dP buffers
-    uint64_t p_full[2], ds_full[2], pd_free[2], drain[2];                          // P and dS buffers
+    uint64_t p_full[2], ds_full[2], pd_free[2], drain[3];                          // P and dS buffers
     uint64_t item_full[kRing], item_empty[kRing];
 };
 
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         misc[0] = 0;
         bar_init(&bars->r_full, 1);
-        bar_init(&bars->r_empty, 1);
+        bar_init(&bars->r_empty, 2);
         bar_init(&bars->land, 1);
         bar_init(&bars->out_full, 1);
         bar_init(&bars->out_free, 16);
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(&bars->p_full[w], 8);
             bar_init(&bars->ds_full[w], 8);
             bar_init(&bars->pd_free[w], 1);
-            bar_init(&bars->drain[w], 1);
         }
+        for (int w = 0; w < 3; ++w) bar_init(&bars->drain[w], 1);
         for (int k = 0; k < kRing; ++k) {
             bar_init(&bars->item_full[k], 1);
             bar_init(&bars->item_empty[k], kWarps);
@@ -252,6 +252,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < x.steps; ++t) {
                     const int s = g % NS;
                     const int2 col = column_of<DKV>(a, x, t);
+                    // dK, dV: lse and D of the columns (negated, lse in log2) go beside the tile
+                    float nl[2], nd[2];
+                    if constexpr (DKV) {
+                        const long long row = win_row_index(a, x.b, col.x, col.y);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const bool in = col.y + lane + 32 * k < a.Nq;
+                            nl[k] = in ? a.lse[row + lane + 32 * k] * -1.4426950408889634f : 0.f;
+                            nd[k] = in ? -a.delta[row + lane + 32 * k] : 0.f;
+                        }
+                    }
                     // dQ: key rows that no row of the item sees are zeroed (0 x NaN would reach dQ)
                     const bool whole = DKV || col.y + kBN <= x.a.s || (col.y >= x.a.lo && col.y + kBN <= x.z.hi);
                     if (lane == 0 && ok) {
@@ -274,8 +285,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) break;
-                    if constexpr (!DKV) {
+                    __syncwarp();
+                    if constexpr (DKV) {
+                        float *ls = reinterpret_cast<float *>(sm + L::kLs) + s * 2 * kBN;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            ls[lane + 32 * k] = nl[k];
+                            ls[kBN + lane + 32 * k] = nd[k];
+                        }
                         __syncwarp();
+                        if (lane == 0) bar_arrive(&bars->ls_full[s]);
+                    } else {
                         if (!whole) {
                             ++land;
                             for (int e = lane; e < kBN * NB * 8; e += 32) {
@@ -301,46 +321,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (r_it > 0) drain_wait(&bars->r_full, (r_it - 1) & 1, W.limit_ns);
             }
             __syncwarp();
-        } else if (warp == 17) {
-            // ------------------------------------------------------------------ lse and D of the columns
-            for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
-                const int it = next_item(item_k);
-                if (it < 0) break;
-                if constexpr (DKV) {
-                    const Item<DKV> x = item_of<DKV>(a, it);
-                    bool ok = true;
-                    for (int t = 0; t < x.steps; ++t) {
-                        const int s = g % NS;
-                        const int2 col = column_of<DKV>(a, x, t);
-                        const long long row = win_row_index(a, x.b, col.x, col.y);
-                        float v[4];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int e = lane + 32 * k;
-                            const bool in = col.y + e < a.Nq;
-                            v[k] = in ? a.lse[row + e] * -1.4426950408889634f : 0.f;
-                            v[2 + k] = in ? -a.delta[row + e] : 0.f;
-                        }
-                        ok = waitw(&bars->c_empty[s], ((g / NS) & 1) ^ 1, W);
-                        if (!ok) break;
-                        float *ls = reinterpret_cast<float *>(sm + L::kLs) + s * 2 * kBN;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            ls[lane + 32 * k] = v[k];
-                            ls[kBN + lane + 32 * k] = v[2 + k];
-                        }
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(&bars->ls_full[s]);
-                        ++g;
-                    }
-                    if (!ok) break;
-                }
-            }
         } else if (lane == 0) {
             // ------------------------------------------------------------------ product issuers
             constexpr uint32_t idesc_s = f16_idesc(kBM, kBN, false), idesc_o = f16_idesc(kBM, D, true);
-            const bool first_products = warp == 18;
-            const uint64_t r1 = sw128_desc(sbase + L::kR1, 16, 1024), r2 = sw128_desc(sbase + L::kR2, 16, 1024);
+            // warp 17: dP, warp 18: S, warp 19: the products of P and dS.  A thread's commits and
+            // waits leave the tensor pipe idle unless another thread's products are queued behind.
+            const bool first_products = warp < 19, is_s = warp == 18;
+            const uint64_t r_desc = sw128_desc(sbase + (is_s ? L::kR1 : L::kR2), 16, 1024);
             uint32_t items = 0;
             bool issued = false;
             for (uint32_t item_k = 0; !*abort_flag; ++item_k) {
@@ -357,29 +344,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = wait1(&bars->r_full, items & 1, W);
                     for (int t = 0; t < steps && ok; ++t, ++g) {
                         const int s = g % NS, w = g % NBUF;
-                        const uint32_t use = ((g / NBUF) & 1) ^ 1;
-                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W) && wait1(&bars->s_free[w], use, W);
+                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W) &&
+                             wait1(is_s ? &bars->s_free[w] : &bars->d_free[w], ((g / NBUF) & 1) ^ 1, W);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t cb = sbase + L::kC + s * 2 * L::kTile;
-                        const uint64_t c1 = sw128_desc(cb, 16, 1024), c2 = sw128_desc(cb + L::kTile, 16, 1024);
+                        const uint64_t c_desc = sw128_desc(sbase + L::kC + s * 2 * L::kTile + (is_s ? 0 : L::kTile), 16, 1024);
+                        const uint32_t dst = tmem + 128 * w + (is_s ? 0 : 64);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t offa = (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
                             const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
-                            mma_bf16(tmem + 128 * w, r1 + offa, c1 + offb, idesc_s, kk > 0);
+                            mma_bf16(dst, r_desc + offa, c_desc + offb, idesc_s, kk > 0);
                         }
-                        mma_commit(&bars->s_full[w]);
-                        ok = wait1(&bars->d_free[w], use, W);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t offa = (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
-                            const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
-                            mma_bf16(tmem + 128 * w + 64, r2 + offa, c2 + offb, idesc_s, kk > 0);
-                        }
-                        mma_commit(&bars->d_full[w]);
+                        mma_commit(is_s ? &bars->s_full[w] : &bars->d_full[w]);
                         if (t == steps - 1) mma_commit(&bars->r_empty);
                     }
                 } else {
@@ -418,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++items;
             }
             if (issued) {   // every product issued completes before TMEM is freed
-                mma_commit(&bars->drain[warp - 18]);
-                drain_wait(&bars->drain[warp - 18], 0, W.limit_ns);
+                mma_commit(&bars->drain[warp - 17]);
+                drain_wait(&bars->drain[warp - 17], 0, W.limit_ns);
             }
         }
         __syncwarp();
