@@ -306,6 +306,13 @@ __device__ __forceinline__ unsigned long long f2add(unsigned long long a, unsign
     return d;
 }
 
+__device__ __forceinline__ unsigned long long f2mul(unsigned long long a, unsigned long long b)
+{
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // A operand from TMEM (P), B from shared memory (V).
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate)
@@ -381,6 +388,83 @@ inline bool bf16_tile_map(CUtensorMap *m, const void *base, long long rows, int 
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Forms on 32-bit shared addresses: a barrier is a base plus a constant, with no 64-bit pointer
+// arithmetic.
+__device__ __forceinline__ bool bar_test(uint32_t b, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(b), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(b), "r"(parity), "r"(kTryNs)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t b)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect_tx(uint32_t b, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], %0;" ::"r"(bytes), "r"(b) : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t b)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(b) : "memory");
+}
+
+__device__ __forceinline__ bool wait_long(uint32_t b, uint32_t parity, const Waiter &w)
+{
+    const unsigned long long t0 = global_ns();
+    while (!bar_try(b, parity)) {
+        if (*w.abort_flag) return false;
+        if (global_ns() - t0 > w.limit_ns) {
+            *w.abort_flag = 1;
+            set_status(w.status, SCOPE_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// Bounded wait by one thread.
+__device__ __forceinline__ bool wait1(uint32_t b, uint32_t parity, const Waiter &w)
+{
+    return bar_try(b, parity) || wait_long(b, parity, w);
+}
+
+// Warp-uniform wait: every lane waits (one instruction for the warp), a vote makes the answer
+// the same for all.
+__device__ __forceinline__ bool waitw(uint32_t b, uint32_t parity, const Waiter &w)
+{
+    return __all_sync(0xffffffffu, bar_try(b, parity) || wait_long(b, parity, w));
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t b, uint32_t parity, unsigned long long limit_ns)
+{
+    const unsigned long long t0 = global_ns();
+    while (!bar_try(b, parity) && global_ns() - t0 < limit_ns) {
+    }
 }
 
 }  // namespace scope

@@ -52,11 +52,11 @@ struct Cols {
     static constexpr int kOut = kPd + 2 * kPdBuf;
     static_assert(kOut + (DKV ? 2 : 1) * D <= (int)kTmemCols, "TMEM columns");
     // column of the bf16 pairs of columns 16 kk .. 16 kk + 15 of P / dS of step g
-    static __device__ __forceinline__ uint32_t p(uint32_t g, int kk)
+    static constexpr __device__ __forceinline__ uint32_t p(uint32_t g, int kk)
     {
         return kShared ? (g % 2) * 128 + (kk >> 1) * 32 + (kk & 1) * 8 : kPd + (g & 1) * kPdBuf + kk * 8;
     }
-    static __device__ __forceinline__ uint32_t ds(uint32_t g, int kk)
+    static constexpr __device__ __forceinline__ uint32_t ds(uint32_t g, int kk)
     {
         return kShared ? p(g, kk) + 64 : kPd + (g & 1) * kPdBuf + (DKV ? 32 : 0) + kk * 8;
     }
@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sbase = smem_u32(sm);
     const Waiter W{abort_flag, a.status, a.wait_ns};
+    const uint32_t bar_base = sbase + L::kBars;
+#define BAR(member) (bar_base + (uint32_t)offsetof(Bars, member))
     int32_t *counter = a.counter + (DKV ? 1 : 0);
 
     if (threadIdx.x == 0) {
@@ -200,18 +202,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t out1 = tmem + T::kOut, out2 = out1 + D;   // dQ or dK; dV
     auto fetch = [&](uint32_t k) -> bool {   // lane 0 of warp 16: the item scheduler
         const int slot = k % kRing;
-        if (!wait1(&bars->item_empty[slot], ((k / kRing) & 1) ^ 1, W)) return false;
+        if (!wait1(BAR(item_empty) + 8u * (slot), ((k / kRing) & 1) ^ 1, W)) return false;
         const int it = atomicAdd(counter, 1);
         ring[slot] = it < n_items ? it : -1;
-        bar_arrive(&bars->item_full[slot]);
+        bar_arrive(BAR(item_full) + 8u * (slot));
         return true;
     };
     auto next_item = [&](uint32_t k) -> int {
         const int slot = k % kRing;
-        if (!waitw(&bars->item_full[slot], (k / kRing) & 1, W)) return -1;
+        if (!waitw(BAR(item_full) + 8u * (slot), (k / kRing) & 1, W)) return -1;
         const int it = ring[slot];
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars->item_empty[slot]);
+        if (lane == 0) bar_arrive(BAR(item_empty) + 8u * (slot));
         if (warp == 16 && it >= 0) {
             int ok = 1;
             if (lane == 0) ok = fetch(k + 1) ? 1 : 0;
@@ -238,13 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (x.steps == 0) continue;
                 int ok = 1;
                 if (lane == 0) {
-                    ok = wait1(&bars->r_empty, (r_it & 1) ^ 1, W);
+                    ok = wait1(BAR(r_empty), (r_it & 1) ^ 1, W);
                     if (ok) {
-                        bar_expect_tx(&bars->r_full, 2 * L::kRows);
+                        bar_expect_tx(BAR(r_full), 2 * L::kRows);
 #pragma unroll
                         for (int k = 0; k < NB; ++k) {
-                            tma_rows(sbase + L::kR1 + k * (kBM * 128), &tmR1, k * 64, x.r0, x.h, x.b, &bars->r_full);
-                            tma_rows(sbase + L::kR2 + k * (kBM * 128), &tmR2, k * 64, x.r0, x.h, x.b, &bars->r_full);
+                            tma_rows(sbase + L::kR1 + k * (kBM * 128), &tmR1, k * 64, x.r0, x.h, x.b, BAR(r_full));
+                            tma_rows(sbase + L::kR2 + k * (kBM * 128), &tmR2, k * 64, x.r0, x.h, x.b, BAR(r_full));
                         }
                         ++r_it;
                     }
@@ -266,9 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // dQ: key rows that no row of the item sees are zeroed (0 x NaN would reach dQ)
                     const bool whole = DKV || col.y + kBN <= x.a.s || (col.y >= x.a.lo && col.y + kBN <= x.z.hi);
                     if (lane == 0 && ok) {
-                        ok = wait1(&bars->c_empty[s], ((g / NS) & 1) ^ 1, W);
+                        ok = wait1(BAR(c_empty) + 8u * (s), ((g / NS) & 1) ^ 1, W);
                         if (ok) {
-                            uint64_t *bar = whole ? &bars->c_full[s] : &bars->land;
+                            const uint32_t bar = whole ? BAR(c_full) + 8u * (s) : BAR(land);
                             bar_expect_tx(bar, 2 * L::kTile);
                             const uint32_t dst = sbase + L::kC + s * 2 * L::kTile;
 #pragma unroll
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             if (!whole) {
                                 landing = true;
-                                ok = wait1(&bars->land, land & 1, W);
+                                ok = wait1(BAR(land), land & 1, W);
                                 landing = !ok;
                             }
                         }
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ls[kBN + lane + 32 * k] = nd[k];
                         }
                         __syncwarp();
-                        if (lane == 0) bar_arrive(&bars->ls_full[s]);
+                        if (lane == 0) bar_arrive(BAR(ls_full) + 8u * (s));
                     } else {
                         if (!whole) {
                             ++land;
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             fence_proxy_async();
                             __syncwarp();
-                            if (lane == 0) bar_arrive(&bars->c_full[s]);
+                            if (lane == 0) bar_arrive(BAR(c_full) + 8u * (s));
                         }
                     }
                     ++g;
@@ -316,9 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) {   // copies already issued land before the CTA exits
                 for (uint32_t v = g > (uint32_t)NS ? g - NS : 0; v < g; ++v)
-                    drain_wait(&bars->c_full[v % NS], (v / NS) & 1, W.limit_ns);
-                if (landing) drain_wait(&bars->land, land & 1, W.limit_ns);
-                if (r_it > 0) drain_wait(&bars->r_full, (r_it - 1) & 1, W.limit_ns);
+                    drain_wait(BAR(c_full) + 8u * (v % NS), (v / NS) & 1, W.limit_ns);
+                if (landing) drain_wait(BAR(land), land & 1, W.limit_ns);
+                if (r_it > 0) drain_wait(BAR(r_full), (r_it - 1) & 1, W.limit_ns);
             }
             __syncwarp();
         } else if (lane == 0) {
@@ -332,20 +334,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool issued = false;
             for (uint32_t item_k = 0; !*abort_flag; ++item_k) {
                 const int slot = item_k % kRing;
-                if (!wait1(&bars->item_full[slot], (item_k / kRing) & 1, W)) break;
+                if (!wait1(BAR(item_full) + 8u * (slot), (item_k / kRing) & 1, W)) break;
                 const int it = ring[slot];
-                bar_arrive(&bars->item_empty[slot]);
+                bar_arrive(BAR(item_empty) + 8u * (slot));
                 if (it < 0) break;
                 const int steps = item_of<DKV>(a, it).steps;
                 if (steps == 0) continue;
                 bool ok = true;
                 issued = true;
                 if (first_products) {
-                    ok = wait1(&bars->r_full, items & 1, W);
+                    ok = wait1(BAR(r_full), items & 1, W);
                     for (int t = 0; t < steps && ok; ++t, ++g) {
                         const int s = g % NS, w = g % NBUF;
-                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W) &&
-                             wait1(is_s ? &bars->s_free[w] : &bars->d_free[w], ((g / NBUF) & 1) ^ 1, W);
+                        ok = wait1(BAR(c_full) + 8u * (s), (g / NS) & 1, W) &&
+                             wait1(is_s ? BAR(s_free) + 8u * (w) : BAR(d_free) + 8u * (w), ((g / NBUF) & 1) ^ 1, W);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t c_desc = sw128_desc(sbase + L::kC + s * 2 * L::kTile + (is_s ? 0 : L::kTile), 16, 1024);
@@ -356,47 +358,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
                             mma_bf16(dst, r_desc + offa, c_desc + offb, idesc_s, kk > 0);
                         }
-                        mma_commit(is_s ? &bars->s_full[w] : &bars->d_full[w]);
-                        if (t == steps - 1) mma_commit(&bars->r_empty);
+                        mma_commit(is_s ? BAR(s_full) + 8u * (w) : BAR(d_full) + 8u * (w));
+                        if (t == steps - 1) mma_commit(BAR(r_empty));
                     }
                 } else {
                     for (int t = 0; t < steps && ok; ++t, ++g) {
                         const int s = g % NS, w = g & 1;
                         const uint32_t use = (g >> 1) & 1;
                         const uint32_t cb = sbase + L::kC + s * 2 * L::kTile;
-                        ok = wait1(&bars->c_full[s], (g / NS) & 1, W);
-                        if (ok && t == 0) ok = wait1(&bars->out_free, (items & 1) ^ 1, W);
+                        ok = wait1(BAR(c_full) + 8u * (s), (g / NS) & 1, W);
+                        if (ok && t == 0) ok = wait1(BAR(out_free), (items & 1) ^ 1, W);
                         if (!ok) break;
                         if constexpr (DKV) {
                             const uint64_t c2 = sw128_desc(cb + L::kTile, kBN * 128, 1024);
-                            ok = wait1(&bars->p_full[w], use, W);
+                            ok = wait1(BAR(p_full) + 8u * (w), use, W);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
                             for (int kk = 0; kk < kBN / 16; ++kk)
                                 mma_bf16_ts(out2, tmem + T::p(g, kk), c2 + (uint64_t)(kk * 2048 >> 4), idesc_o,
                                             (t > 0 || kk > 0) ? 1u : 0u);
-                            if constexpr (T::kShared) mma_commit(&bars->s_free[w]);
+                            if constexpr (T::kShared) mma_commit(BAR(s_free) + 8u * (w));
                         }
                         const uint64_t c1 = sw128_desc(cb, kBN * 128, 1024);
-                        ok = wait1(&bars->ds_full[w], use, W);
+                        ok = wait1(BAR(ds_full) + 8u * (w), use, W);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
                             mma_bf16_ts(out1, tmem + T::ds(g, kk), c1 + (uint64_t)(kk * 2048 >> 4), idesc_o,
                                         (t > 0 || kk > 0) ? 1u : 0u);
-                        mma_commit(T::kShared ? &bars->d_free[w] : &bars->pd_free[w]);
-                        mma_commit(&bars->c_empty[s]);
-                        if (t == steps - 1) mma_commit(&bars->out_full);
+                        mma_commit(T::kShared ? BAR(d_free) + 8u * (w) : BAR(pd_free) + 8u * (w));
+                        mma_commit(BAR(c_empty) + 8u * (s));
+                        if (t == steps - 1) mma_commit(BAR(out_full));
                     }
                 }
                 if (!ok) break;
                 ++items;
             }
             if (issued) {   // every product issued completes before TMEM is freed
-                mma_commit(&bars->drain[warp - 17]);
-                drain_wait(&bars->drain[warp - 17], 0, W.limit_ns);
+                mma_commit(BAR(drain) + 8u * (warp - 17));
+                drain_wait(BAR(drain) + 8u * (warp - 17), 0, W.limit_ns);
             }
         }
         __syncwarp();
@@ -408,11 +410,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wg = (warp >> 2) & 1, odd = warp >> 3, row = threadIdx.x & (kBM - 1);
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         uint32_t items = 0;
+        // the warpgroup's next step, with its buffers and their phases: S / dP buffer w, P / dS
+        // buffer `odd`, column stage s
+        uint32_t mine = odd, w = odd, s = odd, use = 0, pd_use = 0, s_use = 0;
         for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
             const int it = next_item(item_k);
             if (it < 0) break;
             const Item<DKV> x = item_of<DKV>(a, it);
             const bool valid = row < x.nrows;
+            auto below = [&](int e) { return e <= 0 ? 0u : (e >= 32 ? ~0u : (1u << e) - 1u); };
             // what the row sees: columns [0, s) and [lo, hi) (dQ) or [lo, hi) (dK, dV)
             WinRow lim{0, 0, 0};
             float nlse = 0.f, ndelta = 0.f;
@@ -428,18 +434,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ndelta = -a.delta[ix];
                 }
             }
-            const unsigned long long c2 = f2pack(a.scale_log2, a.scale_log2);
+            const unsigned long long c2 = f2pack(a.scale_log2, a.scale_log2), nlse2 = f2pack(nlse, nlse),
+                                     ndelta2 = f2pack(ndelta, ndelta);
             bool ok = true;
-            for (int t = 0; t < x.steps; ++t, ++g) {
-                if ((int)(g & 1) != odd) continue;
-                const int s = g % NS, w = g % NBUF, j0 = column_of<DKV>(a, x, t).y + 32 * wg;
-                const uint32_t use = (g / NBUF) & 1;
+            // this warpgroup's steps: mine, mine + 2, ... below g + steps.  The column tile follows
+            // without a division: position `at` of the query tiles of a head (dK, dV)
+            int at = (int)(mine - g);
+            if constexpr (DKV)
+                while (at >= x.per && x.per > 0) at -= x.per;
+            for (; mine - g < (uint32_t)x.steps; mine += 2) {
+                const int j0 = (DKV ? (x.c0 + at) : x.wt.at((int)(mine - g))) * kBN + 32 * wg;
                 const uint32_t sb = tmem + lane_base + 128 * w + 32 * wg;   // this warpgroup's 32 columns of S
-                auto below = [&](int e) { return e <= 0 ? 0u : (e >= 32 ? ~0u : (1u << e) - 1u); };
-                const uint32_t vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
-                const bool whole = __all_sync(0xffffffffu, vis == ~0u);
-                if constexpr (DKV) ok = waitw(&bars->ls_full[s], (g / NS) & 1, W);
-                ok = ok && waitw(&bars->s_full[w], use, W);
+                const bool whole =
+                    __all_sync(0xffffffffu, j0 + 32 <= lim.s || (lim.lo <= j0 && j0 + 32 <= lim.hi));
+                if constexpr (DKV) ok = waitw(BAR(ls_full) + 8u * s, s_use, W);
+                ok = ok && waitw(BAR(s_full) + 8u * (w), use, W);
                 if (!ok) break;
                 tc_fence_after();
                 float v[32];
@@ -448,23 +457,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!T::kShared) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&bars->s_free[w]);
+                    if (lane == 0) bar_arrive(BAR(s_free) + 8u * (w));
                 }
                 // P of the columns the row sees, 0 elsewhere
                 const float *ls = reinterpret_cast<const float *>(sm + L::kLs) + s * 2 * kBN + 32 * wg;
                 uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
-                    float4 l4 = make_float4(nlse, nlse, nlse, nlse);
-                    if constexpr (DKV) l4 = *reinterpret_cast<const float4 *>(ls + e);
-                    const float2 x0 = f2unpack(f2fma(f2pack(v[e], v[e + 1]), c2, f2pack(l4.x, l4.y)));
-                    const float2 x1 = f2unpack(f2fma(f2pack(v[e + 2], v[e + 3]), c2, f2pack(l4.z, l4.w)));
+                    unsigned long long l0 = nlse2, l1 = nlse2;
+                    if constexpr (DKV) {
+                        const ulonglong2 l4 = *reinterpret_cast<const ulonglong2 *>(ls + e);
+                        l0 = l4.x;
+                        l1 = l4.y;
+                    }
+                    const float2 x0 = f2unpack(f2fma(f2pack(v[e], v[e + 1]), c2, l0));
+                    const float2 x1 = f2unpack(f2fma(f2pack(v[e + 2], v[e + 3]), c2, l1));
                     v[e] = fast_exp2(x0.x);
                     v[e + 1] = fast_exp2(x0.y);
                     v[e + 2] = fast_exp2(x1.x);
                     v[e + 3] = fast_exp2(x1.y);
                 }
                 if (!whole) {
+                    const uint32_t vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0.f;
                 }
@@ -476,17 +490,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[e] = *reinterpret_cast<uint32_t *>(&h2);
                     }
                     if constexpr (!T::kShared) {
-                        ok = waitw(&bars->pd_free[g & 1], ((g >> 1) & 1) ^ 1, W);
+                        ok = waitw(BAR(pd_free) + 8u * odd, pd_use ^ 1, W);
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    tmem_st16(tmem + lane_base + T::p(g, 2 * wg), pk);
+                    tmem_st16(tmem + lane_base + T::p(odd, 2 * wg), pk);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&bars->p_full[g & 1]);
+                    if (lane == 0) bar_arrive(BAR(p_full) + 8u * odd);
                 }
-                ok = waitw(&bars->d_full[w], use, W);
+                ok = waitw(BAR(d_full) + 8u * (w), use, W);
                 if (!ok) break;
                 tc_fence_after();
                 float dv[32];
@@ -495,20 +509,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!T::kShared) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&bars->d_free[w]);
+                    if (lane == 0) bar_arrive(BAR(d_free) + 8u * (w));
                 }
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
-                    float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
-                    if constexpr (DKV) d4 = *reinterpret_cast<const float4 *>(ls + kBN + e);
-                    const float2 x0 = f2unpack(f2add(f2pack(dv[e], dv[e + 1]), f2pack(d4.x, d4.y)));
-                    const float2 x1 = f2unpack(f2add(f2pack(dv[e + 2], dv[e + 3]), f2pack(d4.z, d4.w)));
-                    v[e] *= x0.x;
-                    v[e + 1] *= x0.y;
-                    v[e + 2] *= x1.x;
-                    v[e + 3] *= x1.y;
+                    unsigned long long d0 = ndelta2, d1 = ndelta2;
+                    if constexpr (DKV) {
+                        const ulonglong2 d4 = *reinterpret_cast<const ulonglong2 *>(ls + kBN + e);
+                        d0 = d4.x;
+                        d1 = d4.y;
+                    }
+                    const float2 x0 = f2unpack(f2mul(f2pack(v[e], v[e + 1]), f2add(f2pack(dv[e], dv[e + 1]), d0)));
+                    const float2 x1 = f2unpack(f2mul(f2pack(v[e + 2], v[e + 3]), f2add(f2pack(dv[e + 2], dv[e + 3]), d1)));
+                    v[e] = x0.x;
+                    v[e + 1] = x0.y;
+                    v[e + 2] = x1.x;
+                    v[e + 3] = x1.y;
                 }
                 if (!whole) {   // 0 x what a hidden column holds
+                    const uint32_t vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0.f;
                 }
@@ -518,20 +537,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pk[e] = *reinterpret_cast<uint32_t *>(&h2);
                 }
                 if constexpr (!DKV) {
-                    ok = waitw(&bars->pd_free[g & 1], ((g >> 1) & 1) ^ 1, W);
+                    ok = waitw(BAR(pd_free) + 8u * odd, pd_use ^ 1, W);
                     if (!ok) break;
                     tc_fence_after();
                 }
-                tmem_st16(tmem + lane_base + T::ds(g, 2 * wg), pk);
+                tmem_st16(tmem + lane_base + T::ds(odd, 2 * wg), pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bars->ds_full[g & 1]);
+                if (lane == 0) bar_arrive(BAR(ds_full) + 8u * odd);
+                // the next but one step's buffers and phases
+                pd_use ^= 1;
+                if (NBUF == 2) {
+                    use ^= 1;
+                } else {
+                    w += 2;
+                    if (w >= NBUF) {
+                        w -= NBUF;
+                        use ^= 1;
+                    }
+                }
+                s += 2;
+                if (s >= NS) {
+                    s -= NS;
+                    s_use ^= 1;
+                }
+                if constexpr (DKV) {
+                    at += 2;
+                    while (at >= x.per) at -= x.per;
+                }
             }
+            g += x.steps;
             if (!ok) break;
             // epilogue: of dK and dV half the channels each, of dQ a quarter
             if (x.steps > 0) {
-                if (!waitw(&bars->out_full, items & 1, W)) break;
+                if (!waitw(BAR(out_full), items & 1, W)) break;
                 ++items;
                 tc_fence_after();
             }
@@ -567,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x.steps > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bars->out_free);
+                if (lane == 0) bar_arrive(BAR(out_free));
             }
         }
     }
@@ -642,6 +682,8 @@ cudaError_t backward(const WinArgs &a, cudaStream_t s)
     if (e == cudaSuccess) e = launch_pass<true, D>(a, s);
     return e;
 }
+
+#undef BAR
 
 }  // namespace
 

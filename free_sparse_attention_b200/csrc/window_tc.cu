@@ -130,6 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sbase = smem_u32(sm);
     const Waiter W{abort_flag, a.status, a.wait_ns};
+    const uint32_t bar_base = sbase + L::kBars;
+#define BAR(member) (bar_base + (uint32_t)offsetof(Bars, member))
     const int tiles = (a.Nq + 2 * kBM - 1) / (2 * kBM);
 
     if (threadIdx.x == 0) {
@@ -172,18 +174,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // publishes them in a ring that every warp reads; -1 ends the work.
     auto fetch = [&](uint32_t k) -> bool {
         const int slot = k % kRing;
-        if (!wait1(&bars->item_empty[slot], ((k / kRing) & 1) ^ 1, W)) return false;
+        if (!wait1(BAR(item_empty) + 8u * (slot), ((k / kRing) & 1) ^ 1, W)) return false;
         const int it = atomicAdd(a.counter, 1);
         ring[slot] = it < n_items ? it : -1;
-        bar_arrive(&bars->item_full[slot]);
+        bar_arrive(BAR(item_full) + 8u * (slot));
         return true;
     };
     auto next_item = [&](uint32_t k) -> int {
         const int slot = k % kRing;
-        if (!waitw(&bars->item_full[slot], (k / kRing) & 1, W)) return -1;
+        if (!waitw(BAR(item_full) + 8u * (slot), (k / kRing) & 1, W)) return -1;
         const int it = ring[slot];
         __syncwarp();
-        if (lane == 0) bar_arrive(&bars->item_empty[slot]);
+        if (lane == 0) bar_arrive(BAR(item_empty) + 8u * (slot));
         if (warp == 8 && it >= 0) {
             int ok = 1;
             if (lane == 0) ok = fetch(k + 1) ? 1 : 0;
@@ -207,25 +209,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (x.t0 == x.t1) continue;
                 int ok = 1;
                 if (lane == 0) {
-                    ok = wait1(&bars->q_empty, (q_it & 1) ^ 1, W);
+                    ok = wait1(BAR(q_empty), (q_it & 1) ^ 1, W);
                     if (ok) {
                         const int nq = x.nrows > kBM ? 2 : 1;
-                        bar_expect_tx(&bars->q_full, nq * L::kQTile);
+                        bar_expect_tx(BAR(q_full), nq * L::kQTile);
                         for (int q = 0; q < nq; ++q)
 #pragma unroll
                             for (int b = 0; b < NB; ++b)
                                 tma_rows(sbase + L::kQ + q * L::kQTile + b * (kBM * 128), &tmQ, b * 64, x.r0 + q * kBM, x.h,
-                                         x.b, &bars->q_full);
+                                         x.b, BAR(q_full));
                     }
                     for (int t = x.t0; t < x.t1 && ok; ++t) {
                         const int s = k_it % NS;
-                        ok = wait1(&bars->k_empty[s], ((k_it / NS) & 1) ^ 1, W);
+                        ok = wait1(BAR(k_empty) + 8u * (s), ((k_it / NS) & 1) ^ 1, W);
                         if (!ok) break;
-                        bar_expect_tx(&bars->k_full[s], L::kTile);
+                        bar_expect_tx(BAR(k_full) + 8u * (s), L::kTile);
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
                             tma_rows(sbase + L::kK + s * L::kTile + b * (kBN * 128), &tmK, b * 64, x.all.at(t) * kBN, x.hk, x.b,
-                                     &bars->k_full[s]);
+                                     BAR(k_full) + 8u * (s));
                         ++k_it;
                     }
                     ++q_it;
@@ -235,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) {   // loads already issued land before the CTA exits
                 for (uint32_t v = k_it > (uint32_t)NS ? k_it - NS : 0; v < k_it; ++v)
-                    drain_wait(&bars->k_full[v % NS], (v / NS) & 1, W.limit_ns);
-                if (q_it > 0) drain_wait(&bars->q_full, (q_it - 1) & 1, W.limit_ns);
+                    drain_wait(BAR(k_full) + 8u * (v % NS), (v / NS) & 1, W.limit_ns);
+                if (q_it > 0) drain_wait(BAR(q_full), (q_it - 1) & 1, W.limit_ns);
             }
             __syncwarp();
         } else if (warp == 9) {
@@ -255,16 +257,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // every row of the tile seen by some row of the item: straight to the issuers
                     const bool whole = j0 + kBN <= za.s || (j0 >= za.lo && j0 + kBN <= zz.hi);
                     if (lane == 0) {
-                        ok = wait1(&bars->v_empty[s], ((v_it / NS) & 1) ^ 1, W);
+                        ok = wait1(BAR(v_empty) + 8u * (s), ((v_it / NS) & 1) ^ 1, W);
                         if (ok) {
-                            uint64_t *bar = whole ? &bars->v_full[s] : &bars->v_land;
+                            const uint32_t bar = whole ? BAR(v_full) + 8u * (s) : BAR(v_land);
                             bar_expect_tx(bar, L::kTile);
 #pragma unroll
                             for (int b = 0; b < NB; ++b)
                                 tma_rows(dst + b * (kBN * 128), &tmV, b * 64, j0, x.hk, x.b, bar);
                             if (!whole) {
                                 landing = true;
-                                ok = wait1(&bars->v_land, land & 1, W);
+                                ok = wait1(BAR(v_land), land & 1, W);
                                 landing = !ok;
                             }
                         }
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         fence_proxy_async();
                         __syncwarp();
-                        if (lane == 0) bar_arrive(&bars->v_full[s]);
+                        if (lane == 0) bar_arrive(BAR(v_full) + 8u * (s));
                     }
                     ++v_it;
                 }
@@ -291,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0)
                 for (uint32_t v = v_it > (uint32_t)NS ? v_it - NS : 0; v < v_it; ++v)
-                    drain_wait(&bars->v_full[v % NS], (v / NS) & 1, W.limit_ns);
-            if (lane == 0 && landing) drain_wait(&bars->v_land, land & 1, W.limit_ns);
+                    drain_wait(BAR(v_full) + 8u * (v % NS), (v / NS) & 1, W.limit_ns);
+            if (lane == 0 && landing) drain_wait(BAR(v_land), land & 1, W.limit_ns);
             __syncwarp();
         } else {
             // -------------------------------------------------------------- product issuers
@@ -305,20 +307,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t qd = sw128_desc(sbase + L::kQ + q * L::kQTile, 16, 1024);
                 for (uint32_t item_k = 0; !*abort_flag; ++item_k) {
                     const int slot = item_k % kRing;
-                    if (!wait1(&bars->item_full[slot], (item_k / kRing) & 1, W)) break;
+                    if (!wait1(BAR(item_full) + 8u * (slot), (item_k / kRing) & 1, W)) break;
                     const int it = ring[slot];
-                    bar_arrive(&bars->item_empty[slot]);
+                    bar_arrive(BAR(item_empty) + 8u * (slot));
                     if (it < 0) break;
                     const Item x = item_of(a, it, tiles);
                     if (x.t0 == x.t1) continue;
-                    if (!wait1(&bars->q_full, q_it & 1, W)) break;
+                    if (!wait1(BAR(q_full), q_it & 1, W)) break;
                     ++q_it;
                     issued = true;
                     const WinTiles mine = pick(q == 1, x.q);
                     int ns = 0, np = 0;   // S tiles and P V products issued for this Q tile
                     auto qk_step = [&](int t) -> bool {
                         const int ks = k_it % NS;
-                        if (!wait1(&bars->k_full[ks], (k_it / NS) & 1, W)) return false;
+                        if (!wait1(BAR(k_full) + 8u * (ks), (k_it / NS) & 1, W)) return false;
                         if (sees(mine, x.all.at(t))) {
                             tc_fence_after();
                             const uint64_t kd = sw128_desc(sbase + L::kK + ks * L::kTile, 16, 1024);
@@ -329,11 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
                                 mma_bf16(s_base + buf * kBN, qd + offa, kd + offb, idesc_qk, kk > 0);
                             }
-                            mma_commit(&bars->s_full[q][buf]);
+                            mma_commit(BAR(s_full) + 8u * (kMaxSB * (q) + (buf)));
                             ++ns;
                         }
-                        mma_commit(&bars->k_empty[ks]);
-                        if (t == x.t1 - 1) mma_commit(&bars->q_empty);
+                        mma_commit(BAR(k_empty) + 8u * (ks));
+                        if (t == x.t1 - 1) mma_commit(BAR(q_empty));
                         ++k_it;
                         return true;
                     };
@@ -341,12 +343,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int t = x.t0; t < min(x.t0 + NSB, x.t1) && ok; ++t) ok = qk_step(t);
                     for (int t = x.t0; t < x.t1 && ok; ++t) {
                         const int vs = v_it % NS;
-                        ok = wait1(&bars->v_full[vs], (v_it / NS) & 1, W);
+                        ok = wait1(BAR(v_full) + 8u * (vs), (v_it / NS) & 1, W);
                         if (ok && sees(mine, x.all.at(t))) {
                             const int buf = np % NSB;
-                            ok = wait1(&bars->p_full[q][buf], (p_par >> buf) & 1u, W);
+                            ok = wait1(BAR(p_full) + 8u * (kMaxSB * (q) + (buf)), (p_par >> buf) & 1u, W);
                             if (ok && np == 0) {
-                                ok = wait1(&bars->o_free[q], (o_items & 1) ^ 1, W);
+                                ok = wait1(BAR(o_free) + 8u * (q), (o_items & 1) ^ 1, W);
                                 ++o_items;
                             }
                             if (ok) {
@@ -357,20 +359,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int kk = 0; kk < kBN / 16; ++kk)
                                     mma_bf16_ts(o_tm, s_base + buf * kBN + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), idesc_pv,
                                                 (np > 0 || kk > 0) ? 1u : 0u);
-                                mma_commit(&bars->o_done[q][buf]);
+                                mma_commit(BAR(o_done) + 8u * (kMaxSB * (q) + (buf)));
                                 ++np;
                             }
                         }
                         if (!ok) break;
-                        mma_commit(&bars->v_empty[vs]);
+                        mma_commit(BAR(v_empty) + 8u * (vs));
                         ++v_it;
                         if (t + NSB < x.t1) ok = qk_step(t + NSB);
                     }
                     if (!ok) break;
                 }
                 if (issued) {   // every product issued completes before TMEM is freed
-                    mma_commit(&bars->drain[q]);
-                    drain_wait(&bars->drain[q], 0, W.limit_ns);
+                    mma_commit(BAR(drain) + 8u * (q));
+                    drain_wait(BAR(drain) + 8u * (q), 0, W.limit_ns);
                 }
             }
             __syncwarp();
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kt = x.all.at(t);
                 if (!sees(mine, kt)) continue;
                 const int b = n % NSB, j0 = kt * kBN;
-                ok = waitw(&bars->s_full[q][b], (s_par >> b) & 1u, W);
+                ok = waitw(BAR(s_full) + 8u * (kMaxSB * (q) + (b)), (s_par >> b) & 1u, W);
                 if (!ok) break;
                 s_par ^= 1u << b;
                 tc_fence_after();
@@ -411,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int h = 0; h < kBN / 32; ++h) tmem_ld32(tmem + lane_base + sb_col + h * 32, s + h * 32);
                 tmem_wait_ld();
                 if (!win_all(first_row, last_row, j0, j0 + kBN)) {
+                    asm volatile("" ::: "memory");   // a branch, not 64 selects on every tile
                     // bit j: whether the row sees key j0 + j
                     auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
                     const unsigned long long vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // more than 8 (P <= 2^8, sums in fp32); -inf until the row has seen a key
                 const bool need = mt > m_run + 8.f;
                 if (n > 0 && __any_sync(0xffffffffu, need)) {
-                    ok = waitw(&bars->o_done[q][(n - 1) % NSB], pv_parity(n - 1), W);
+                    ok = waitw(BAR(o_done) + 8u * (kMaxSB * (q) + ((n - 1) % NSB)), pv_parity(n - 1), W);
                     if (!ok) break;
                     tc_fence_after();
                     const float alpha = need ? fast_exp2(m_run - mt) : 1.f;
@@ -471,12 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bars->p_full[q][b]);
+                if (lane == 0) bar_arrive(BAR(p_full) + 8u * (kMaxSB * (q) + (b)));
                 ++n;
             }
             if (!ok) break;
             if (n > 0) {
-                if (!waitw(&bars->o_done[q][(n - 1) % NSB], pv_parity(n - 1), W)) break;
+                if (!waitw(BAR(o_done) + 8u * (kMaxSB * (q) + ((n - 1) % NSB)), pv_parity(n - 1), W)) break;
 #pragma unroll
                 for (int b = 0; b < NSB; ++b) o_par ^= (uint32_t)(((n + NSB - 1 - b) / NSB) & 1) << b;
                 tc_fence_after();
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bars->o_free[q]);
+                if (lane == 0) bar_arrive(BAR(o_free) + 8u * (q));
             }
         }
     }
@@ -552,6 +555,8 @@ cudaError_t launch_forward(const WinArgs &a, cudaStream_t s)
     window_tc_kernel<D><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(tq, tk, tv, a, (int)items);
     return cudaGetLastError();
 }
+
+#undef BAR
 
 }  // namespace
 

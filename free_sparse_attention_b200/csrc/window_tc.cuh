@@ -4,15 +4,17 @@
 #include "tc_common.cuh"
 #include "window.cuh"
 
+#include <cstddef>
+
 namespace scope {
 
 // 4-D tile (64 channels x rows of one head) of a strided [B, heads, N, d] tensor.
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *tm, int c, int n, int h, int b, uint64_t *bar)
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *tm, int c, int n, int h, int b, uint32_t bar)
 {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c), "r"(n), "r"(h), "r"(b), "r"(smem_u32(bar))
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c), "r"(n), "r"(h), "r"(b), "r"(bar)
         : "memory");
 }
 
