@@ -21,7 +21,8 @@ struct WinArgs {
     void *O;                     // forward output; backward: the forward's output (read)
     void *dQ, *dK, *dV;
     float *lse;                  // [B, H, Nq] natural log, or NULL (forward); read in backward
-    float *delta;                // [B, H, Nq] rowsum(G o O) (backward workspace)
+    float *delta, *nlse;         // [B, H, Nq] rowsum(G o O), negated in the bf16 form, and (bf16)
+                                 // -lse log2 e (backward workspace)
     WinLayout lq, lk, lv, lo, lg, ldq, ldk, ldv;
     const int32_t *q_first;      // [B] or NULL: position of each entry's first query
     const int32_t *k_len;        // [B] or NULL: keys of each entry

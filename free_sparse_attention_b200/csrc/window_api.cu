@@ -187,7 +187,7 @@ Plan plan_of(const scope_window_params &p)
 }
 
 struct WinWs {
-    size_t part_o, part_lse, delta, total;
+    size_t part_o, part_lse, delta, nlse, total;
 };
 
 WinWs ws_of(const scope_window_params &p)
@@ -201,7 +201,8 @@ WinWs ws_of(const scope_window_params &p)
     w.part_lse = o;
     if (pl.splits > 1) o = align_up(o + sizeof(float) * rows * pl.splits);
     w.delta = kHeader;   // the backward pass has the partials' place to itself
-    w.total = std::max(o, align_up(kHeader + sizeof(float) * rows));
+    w.nlse = align_up(w.delta + sizeof(float) * rows);
+    w.total = std::max(o, p.dtype == SCOPE_BF16 ? align_up(w.nlse + sizeof(float) * rows) : w.nlse);
     return w;
 }
 
@@ -238,6 +239,7 @@ scope_status window_args(const scope_window_params &p, const scope_window_layout
     a.part_o = reinterpret_cast<float *>(base + w.part_o);
     a.part_lse = reinterpret_cast<float *>(base + w.part_lse);
     a.delta = reinterpret_cast<float *>(base + w.delta);
+    a.nlse = reinterpret_cast<float *>(base + w.nlse);
     a.scale = (float)(1.0 / std::sqrt((double)p.d));
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)p.d));
     a.status = reinterpret_cast<int32_t *>(base);

@@ -9,11 +9,10 @@
 //            rows R1, R2   columns C1, C2   S = R1 C1^T  dP = R2 C2^T   results
 //   dQ       Q, dO         K, V             S            dP             dQ += dS C1
 //   dK, dV   K, V          Q, dO            S^T          dP^T           dK += dS C1, dV += P C2
-// Per CTA (persistent, one per SM): warps 0-15 turn S and dP into P and dS, two warpgroups (thread
-// r of each owns row r = TMEM lane r, one 32 of the columns) for even and two for odd steps; warp 16
-// loads rows and column tiles by TMA (and lse and D of the columns, for dK, dV) and hands out the
-// items; warps 18 and 17 issue S and dP, warp 19 the products of P and dS, read as operands from
-// TMEM.
+// Per CTA (persistent, one per SM): warps 0-3 / 4-7 turn S and dP of even / odd steps into P and
+// dS (thread r owns row r = TMEM lane r); warp 8 loads rows and column tiles by TMA (and lse and D
+// of the columns, for dK, dV) and hands out the items; warps 10 and 9 issue S and dP, warp 11 the
+// products of P and dS, read as operands from TMEM.
 // What bounds a step is the chain product -> commit -> wait -> arithmetic -> arrive -> product
 // (about 3500 cycles when one buffer goes through all of it), so the chain is cut where TMEM has
 // room: S and dP are released as soon as they are in registers, P and dS have columns of their
@@ -27,9 +26,9 @@ namespace scope {
 namespace {
 
 constexpr int kBM = 128, kBN = 64;
-constexpr int kWarps = 20, kThreads = kWarps * 32;
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kOtherRegs = 64;   // 65536 / 640, a multiple of 8
-static_assert(4 * kSoftmaxRegs + kOtherRegs == 5 * kLaunchRegs, "register split");
+constexpr int kWarps = 12, kThreads = kWarps * 32;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;   // 65536 / 384, a multiple of 8
+static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "register split");
 constexpr int kMaxStages = 8, kMaxBuf = 3, kRing = 4;
 constexpr uint32_t kTmemCols = 512;
 
@@ -136,6 +135,23 @@ __device__ __forceinline__ int2 column_of(const WinArgs &a, const Item<DKV> &x, 
     return make_int2(x.h / (a.H / a.Hkv), x.wt.at(t) * kBN);
 }
 
+// 32 values of this thread's row as bf16 pairs in 16 TMEM columns.
+__device__ __forceinline__ void store_half(uint32_t taddr, const float *v)
+{
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        pk[e] = *reinterpret_cast<uint32_t *>(&h2);
+    }
+    tmem_st16(taddr, pk);
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float *src, bool in)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+
 template <bool DKV, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmR1, const __grid_constant__ CUtensorMap tmR2,
@@ -165,21 +181,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&bars->r_empty, 2);
         bar_init(&bars->land, 1);
         bar_init(&bars->out_full, 1);
-        bar_init(&bars->out_free, 16);
+        bar_init(&bars->out_free, 8);
         for (int s = 0; s < kMaxStages; ++s) {
             bar_init(&bars->c_full[s], 1);
             bar_init(&bars->c_empty[s], 1);
-            bar_init(&bars->ls_full[s], 1);
+            bar_init(&bars->ls_full[s], 32);
         }
         for (int w = 0; w < kMaxBuf; ++w) {
             bar_init(&bars->s_full[w], 1);
             bar_init(&bars->d_full[w], 1);
-            bar_init(&bars->s_free[w], T::kShared ? 1 : 8);   // the product's commit, or the 8 warps
-            bar_init(&bars->d_free[w], T::kShared ? 1 : 8);
+            bar_init(&bars->s_free[w], T::kShared ? 1 : 4);   // the product's commit, or the 4 warps
+            bar_init(&bars->d_free[w], T::kShared ? 1 : 4);
         }
         for (int w = 0; w < 2; ++w) {
-            bar_init(&bars->p_full[w], 8);
-            bar_init(&bars->ds_full[w], 8);
+            bar_init(&bars->p_full[w], 4);
+            bar_init(&bars->ds_full[w], 4);
             bar_init(&bars->pd_free[w], 1);
         }
         for (int w = 0; w < 3; ++w) bar_init(&bars->drain[w], 1);
@@ -189,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 18) {
+    if (warp == 10) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");
@@ -200,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t out1 = tmem + T::kOut, out2 = out1 + D;   // dQ or dK; dV
-    auto fetch = [&](uint32_t k) -> bool {   // lane 0 of warp 16: the item scheduler
+    auto fetch = [&](uint32_t k) -> bool {   // lane 0 of warp 8: the item scheduler
         const int slot = k % kRing;
         if (!wait1(BAR(item_empty) + 8u * (slot), ((k / kRing) & 1) ^ 1, W)) return false;
         const int it = atomicAdd(counter, 1);
@@ -214,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int it = ring[slot];
         __syncwarp();
         if (lane == 0) bar_arrive(BAR(item_empty) + 8u * (slot));
-        if (warp == 16 && it >= 0) {
+        if (warp == 8 && it >= 0) {
             int ok = 1;
             if (lane == 0) ok = fetch(k + 1) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -222,14 +238,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return it;
     };
-    if (warp == 16 && lane == 0) fetch(0);
+    if (warp == 8 && lane == 0) fetch(0);
 
     // Every role counts the CTA's steps in g: step g uses S / dP buffer g % NBUF, P / dS buffer
     // g % 2 and column stage g % NS; phase parities follow from the quotients.
     uint32_t g = 0;
-    if (warp >= 16) {
+    if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 16) {
+        if (warp == 8) {
             // ------------------------------------------------------------------ loads
             uint32_t r_it = 0, land = 0;
             bool landing = false;
@@ -254,17 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < x.steps; ++t) {
                     const int s = g % NS;
                     const int2 col = column_of<DKV>(a, x, t);
-                    // dK, dV: lse and D of the columns (negated, lse in log2) go beside the tile
-                    float nl[2], nd[2];
-                    if constexpr (DKV) {
-                        const long long row = win_row_index(a, x.b, col.x, col.y);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const bool in = col.y + lane + 32 * k < a.Nq;
-                            nl[k] = in ? a.lse[row + lane + 32 * k] * -1.4426950408889634f : 0.f;
-                            nd[k] = in ? -a.delta[row + lane + 32 * k] : 0.f;
-                        }
-                    }
                     // dQ: key rows that no row of the item sees are zeroed (0 x NaN would reach dQ)
                     const bool whole = DKV || col.y + kBN <= x.a.s || (col.y >= x.a.lo && col.y + kBN <= x.z.hi);
                     if (lane == 0 && ok) {
@@ -289,14 +294,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     __syncwarp();
                     if constexpr (DKV) {
-                        float *ls = reinterpret_cast<float *>(sm + L::kLs) + s * 2 * kBN;
+                        // -lse log2 e and -D of the columns beside the tile; the copies arrive on
+                        // the barrier themselves
+                        const uint32_t ls = sbase + L::kLs + s * (2 * kBN * 4) + lane * 4;
+                        const long long row = win_row_index(a, x.b, col.x, col.y) + lane;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            ls[lane + 32 * k] = nl[k];
-                            ls[kBN + lane + 32 * k] = nd[k];
+                            const bool in = col.y + lane + 32 * k < a.Nq;
+                            cp_async4(ls + 128 * k, a.nlse + (in ? row + 32 * k : 0), in);
+                            cp_async4(ls + kBN * 4 + 128 * k, a.delta + (in ? row + 32 * k : 0), in);
                         }
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(BAR(ls_full) + 8u * (s));
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(BAR(ls_full) + 8u * s) : "memory");
                     } else {
                         if (!whole) {
                             ++land;
@@ -316,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
             }
+            asm volatile("cp.async.wait_all;\n" ::: "memory");
             if (lane == 0) {   // copies already issued land before the CTA exits
                 for (uint32_t v = g > (uint32_t)NS ? g - NS : 0; v < g; ++v)
                     drain_wait(BAR(c_full) + 8u * (v % NS), (v / NS) & 1, W.limit_ns);
@@ -326,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (lane == 0) {
             // ------------------------------------------------------------------ product issuers
             constexpr uint32_t idesc_s = f16_idesc(kBM, kBN, false), idesc_o = f16_idesc(kBM, D, true);
-            // warp 17: dP, warp 18: S, warp 19: the products of P and dS.  A thread's commits and
+            // warp 9: dP, warp 10: S, warp 11: the products of P and dS.  A thread's commits and
             // waits leave the tensor pipe idle unless another thread's products are queued behind.
-            const bool first_products = warp < 19, is_s = warp == 18;
+            const bool first_products = warp < 11, is_s = warp == 10;
             const uint64_t r_desc = sw128_desc(sbase + (is_s ? L::kR1 : L::kR2), 16, 1024);
             uint32_t items = 0;
             bool issued = false;
@@ -397,17 +406,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++items;
             }
             if (issued) {   // every product issued completes before TMEM is freed
-                mma_commit(BAR(drain) + 8u * (warp - 17));
-                drain_wait(BAR(drain) + 8u * (warp - 17), 0, W.limit_ns);
+                mma_commit(BAR(drain) + 8u * (warp - 9));
+                drain_wait(BAR(drain) + 8u * (warp - 9), 0, W.limit_ns);
             }
         }
         __syncwarp();
     } else {
         // ---------------------------------------------------------------------- P and dS, epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        // warpgroup: column half, and the parity of its steps (two steps in work at a time hide the
-        // latencies of each other's barriers and TMEM accesses)
-        const int wg = (warp >> 2) & 1, odd = warp >> 3, row = threadIdx.x & (kBM - 1);
+        // the warpgroup's steps are those of its parity: two steps in work at a time
+        const int odd = warp >> 2, row = threadIdx.x & (kBM - 1);
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         uint32_t items = 0;
         // the warpgroup's next step, with its buffers and their phases: S / dP buffer w, P / dS
@@ -418,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it < 0) break;
             const Item<DKV> x = item_of<DKV>(a, it);
             const bool valid = row < x.nrows;
-            auto below = [&](int e) { return e <= 0 ? 0u : (e >= 32 ? ~0u : (1u << e) - 1u); };
+            auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
             // what the row sees: columns [0, s) and [lo, hi) (dQ) or [lo, hi) (dK, dV)
             WinRow lim{0, 0, 0};
             float nlse = 0.f, ndelta = 0.f;
@@ -430,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     lim = win_row(a, x.first + x.r0 + row, x.kl);
                     const long long ix = win_row_index(a, x.b, x.h, x.r0 + row);
-                    nlse = a.lse[ix] * -1.4426950408889634f;
-                    ndelta = -a.delta[ix];
+                    nlse = a.nlse[ix];
+                    ndelta = a.delta[ix];
                 }
             }
             const unsigned long long c2 = f2pack(a.scale_log2, a.scale_log2), nlse2 = f2pack(nlse, nlse),
@@ -443,27 +451,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (DKV)
                 while (at >= x.per && x.per > 0) at -= x.per;
             for (; mine - g < (uint32_t)x.steps; mine += 2) {
-                const int j0 = (DKV ? (x.c0 + at) : x.wt.at((int)(mine - g))) * kBN + 32 * wg;
-                const uint32_t sb = tmem + lane_base + 128 * w + 32 * wg;   // this warpgroup's 32 columns of S
+                const int j0 = (DKV ? (x.c0 + at) : x.wt.at((int)(mine - g))) * kBN;
+                const uint32_t sb = tmem + lane_base + 128 * w;   // S; dP at + 64
                 const bool whole =
-                    __all_sync(0xffffffffu, j0 + 32 <= lim.s || (lim.lo <= j0 && j0 + 32 <= lim.hi));
+                    __all_sync(0xffffffffu, j0 + kBN <= lim.s || (lim.lo <= j0 && j0 + kBN <= lim.hi));
                 if constexpr (DKV) ok = waitw(BAR(ls_full) + 8u * s, s_use, W);
-                ok = ok && waitw(BAR(s_full) + 8u * (w), use, W);
+                ok = ok && waitw(BAR(s_full) + 8u * w, use, W);
                 if (!ok) break;
                 tc_fence_after();
-                float v[32];
+                float v[kBN];
                 tmem_ld32(sb, v);
+                tmem_ld32(sb + 32, v + 32);
                 tmem_wait_ld();
                 if constexpr (!T::kShared) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(BAR(s_free) + 8u * (w));
+                    if (lane == 0) bar_arrive(BAR(s_free) + 8u * w);
                 }
                 // P of the columns the row sees, 0 elsewhere
-                const float *ls = reinterpret_cast<const float *>(sm + L::kLs) + s * 2 * kBN + 32 * wg;
-                uint32_t pk[16];
+                const float *ls = reinterpret_cast<const float *>(sm + L::kLs) + s * 2 * kBN;
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
+                for (int e = 0; e < kBN; e += 4) {
                     unsigned long long l0 = nlse2, l1 = nlse2;
                     if constexpr (DKV) {
                         const ulonglong2 l4 = *reinterpret_cast<const ulonglong2 *>(ls + e);
@@ -477,42 +485,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[e + 2] = fast_exp2(x1.x);
                     v[e + 3] = fast_exp2(x1.y);
                 }
+                unsigned long long vis = ~0ull;
                 if (!whole) {
-                    const uint32_t vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
+                    vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0.f;
+                    for (int e = 0; e < kBN; ++e) v[e] = (vis >> e) & 1ull ? v[e] : 0.f;
                 }
                 if constexpr (DKV) {
-                    // the shared buffers: this half's 16 columns lie under its own 32 of S
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-                        pk[e] = *reinterpret_cast<uint32_t *>(&h2);
-                    }
                     if constexpr (!T::kShared) {
                         ok = waitw(BAR(pd_free) + 8u * odd, pd_use ^ 1, W);
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    tmem_st16(tmem + lane_base + T::p(odd, 2 * wg), pk);
+                    store_half(tmem + lane_base + T::p(odd, 0), v);
+                    store_half(tmem + lane_base + T::p(odd, 2), v + 32);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive(BAR(p_full) + 8u * odd);
                 }
-                ok = waitw(BAR(d_full) + 8u * (w), use, W);
+                ok = waitw(BAR(d_full) + 8u * w, use, W);
                 if (!ok) break;
                 tc_fence_after();
-                float dv[32];
+                float dv[kBN];
                 tmem_ld32(sb + 64, dv);
+                tmem_ld32(sb + 96, dv + 32);
                 tmem_wait_ld();
                 if constexpr (!T::kShared) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(BAR(d_free) + 8u * (w));
+                    if (lane == 0) bar_arrive(BAR(d_free) + 8u * w);
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
+                for (int e = 0; e < kBN; e += 4) {
                     unsigned long long d0 = ndelta2, d1 = ndelta2;
                     if constexpr (DKV) {
                         const ulonglong2 d4 = *reinterpret_cast<const ulonglong2 *>(ls + kBN + e);
@@ -527,21 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[e + 3] = x1.y;
                 }
                 if (!whole) {   // 0 x what a hidden column holds
-                    const uint32_t vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1u ? v[e] : 0.f;
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-                    pk[e] = *reinterpret_cast<uint32_t *>(&h2);
+                    for (int e = 0; e < kBN; ++e) v[e] = (vis >> e) & 1ull ? v[e] : 0.f;
                 }
                 if constexpr (!DKV) {
                     ok = waitw(BAR(pd_free) + 8u * odd, pd_use ^ 1, W);
                     if (!ok) break;
                     tc_fence_after();
                 }
-                tmem_st16(tmem + lane_base + T::ds(odd, 2 * wg), pk);
+                store_half(tmem + lane_base + T::ds(odd, 0), v);
+                store_half(tmem + lane_base + T::ds(odd, 2), v + 32);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -569,18 +569,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             g += x.steps;
             if (!ok) break;
-            // epilogue: of dK and dV half the channels each, of dQ a quarter
+            // epilogue: dK by warpgroup 0 and dV by 1; of dQ, half the channels each
             if (x.steps > 0) {
                 if (!waitw(BAR(out_full), items & 1, W)) break;
                 ++items;
                 tc_fence_after();
             }
-            constexpr int CH = DKV ? D / 2 : D / 4;   // channels of one warpgroup
-            const int ch0 = DKV ? odd * CH : (2 * wg + odd) * CH;
-            const uint32_t src = (DKV && wg == 1 ? out2 : out1) + lane_base + ch0;
-            const float scale = DKV && wg == 1 ? 1.f : a.scale;
-            const WinLayout lay = DKV ? (wg ? a.ldv : a.ldk) : a.ldq;
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(DKV ? (wg ? a.dV : a.dK) : a.dQ) + x.b * lay.b + x.h * lay.h +
+            constexpr int CH = DKV ? D : D / 2;   // channels of one warpgroup
+            const int ch0 = DKV ? 0 : odd * CH;
+            const uint32_t src = (DKV && odd ? out2 : out1) + lane_base + ch0;
+            const float scale = DKV && odd ? 1.f : a.scale;
+            const WinLayout lay = DKV ? (odd ? a.ldv : a.ldk) : a.ldq;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(DKV ? (odd ? a.dV : a.dK) : a.dQ) + x.b * lay.b + x.h * lay.h +
                                  (x.r0 + row) * lay.n + ch0;
 #pragma unroll 1
             for (int h = 0; h < CH / 16; ++h) {
@@ -614,11 +614,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 18)
+    if (warp == 10)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-// D_i = dO_i . O_i, D / 8 threads per row; clears the status word and the item counters first
+// -D_i = -dO_i . O_i and -lse_i log2 e for the two passes, D / 8 threads per row; clears the status word and the item counters first
 // (this launch precedes the two kernels above on the stream).
 template <int D>
 __global__ void __launch_bounds__(256) window_delta_kernel(WinArgs a)
@@ -646,7 +646,10 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WinArgs a)
     }
 #pragma unroll
     for (int x = TPR / 2; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    if (g == 0 && row < rows) a.delta[row] = s;
+    if (g == 0 && row < rows) {
+        a.delta[row] = -s;
+        a.nlse[row] = a.lse[row] * -1.4426950408889634f;
+    }
 }
 
 template <bool DKV, int D>
