@@ -448,17 +448,30 @@ __device__ __forceinline__ bool wait_long(uint32_t b, uint32_t parity, const Wai
     return true;
 }
 
+// One arrival for the warp, by lane 0, without a branch.
+__device__ __forceinline__ void warp_arrive(uint32_t b, int lane)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.eq.s32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(b),
+        "r"(lane)
+        : "memory");
+}
+
 // Bounded wait by one thread.
 __device__ __forceinline__ bool wait1(uint32_t b, uint32_t parity, const Waiter &w)
 {
-    return bar_test(b, parity) || wait_long(b, parity, w);   // a test takes half a try's time
+    if (__builtin_expect(bar_test(b, parity), 1)) return true;   // a test takes half a try's time
+    return wait_long(b, parity, w);
 }
 
 // Warp-uniform wait: every lane waits (one instruction for the warp), a vote makes the answer
 // the same for all.
 __device__ __forceinline__ bool waitw(uint32_t b, uint32_t parity, const Waiter &w)
 {
-    return __all_sync(0xffffffffu, bar_test(b, parity) || wait_long(b, parity, w));
+    if (__builtin_expect(__all_sync(0xffffffffu, bar_test(b, parity)), 1)) return true;
+    return __all_sync(0xffffffffu, wait_long(b, parity, w));
 }
 
 __device__ __forceinline__ void drain_wait(uint32_t b, uint32_t parity, unsigned long long limit_ns)

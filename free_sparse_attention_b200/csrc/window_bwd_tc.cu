@@ -450,14 +450,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             int at = (int)(mine - g);
             if constexpr (DKV)
                 while (at >= x.per && x.per > 0) at -= x.per;
-            for (; mine - g < (uint32_t)x.steps; mine += 2) {
+            for (; ok && mine - g < (uint32_t)x.steps; mine += 2) {
                 const int j0 = (DKV ? (x.c0 + at) : x.wt.at((int)(mine - g))) * kBN;
                 const uint32_t sb = tmem + lane_base + 128 * w;   // S; dP at + 64
                 const bool whole =
                     __all_sync(0xffffffffu, j0 + kBN <= lim.s || (lim.lo <= j0 && j0 + kBN <= lim.hi));
-                if constexpr (DKV) ok = waitw(BAR(ls_full) + 8u * s, s_use, W);
-                ok = ok && waitw(BAR(s_full) + 8u * w, use, W);
-                if (!ok) break;
+                // a wait that gave up leaves the loop at the end of the step: what the step computes
+                // from then on goes nowhere, and nothing else waits for long
+                if constexpr (DKV) ok &= waitw(BAR(ls_full) + 8u * s, s_use, W);
+                ok &= waitw(BAR(s_full) + 8u * w, use, W);
                 tc_fence_after();
                 float v[kBN];
                 tmem_ld32(sb, v);
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!T::kShared) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(BAR(s_free) + 8u * w);
+                    warp_arrive(BAR(s_free) + 8u * w, lane);
                 }
                 // P of the columns the row sees, 0 elsewhere
                 const float *ls = reinterpret_cast<const float *>(sm + L::kLs) + s * 2 * kBN;
@@ -486,15 +487,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[e + 3] = fast_exp2(x1.y);
                 }
                 unsigned long long vis = ~0ull;
-                if (!whole) {
+                if (__builtin_expect(!whole, 0)) {
                     vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
 #pragma unroll
                     for (int e = 0; e < kBN; ++e) v[e] = (vis >> e) & 1ull ? v[e] : 0.f;
                 }
                 if constexpr (DKV) {
                     if constexpr (!T::kShared) {
-                        ok = waitw(BAR(pd_free) + 8u * odd, pd_use ^ 1, W);
-                        if (!ok) break;
+                        ok &= waitw(BAR(pd_free) + 8u * odd, pd_use ^ 1, W);
                         tc_fence_after();
                     }
                     store_half(tmem + lane_base + T::p(odd, 0), v);
@@ -502,10 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(BAR(p_full) + 8u * odd);
+                    warp_arrive(BAR(p_full) + 8u * odd, lane);
                 }
-                ok = waitw(BAR(d_full) + 8u * w, use, W);
-                if (!ok) break;
+                ok &= waitw(BAR(d_full) + 8u * w, use, W);
                 tc_fence_after();
                 float dv[kBN];
                 tmem_ld32(sb + 64, dv);
@@ -514,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!T::kShared) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(BAR(d_free) + 8u * w);
+                    warp_arrive(BAR(d_free) + 8u * w, lane);
                 }
 #pragma unroll
                 for (int e = 0; e < kBN; e += 4) {
@@ -531,13 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[e + 2] = x1.x;
                     v[e + 3] = x1.y;
                 }
-                if (!whole) {   // 0 x what a hidden column holds
+                if (__builtin_expect(!whole, 0)) {   // 0 x what a hidden column holds
 #pragma unroll
                     for (int e = 0; e < kBN; ++e) v[e] = (vis >> e) & 1ull ? v[e] : 0.f;
                 }
                 if constexpr (!DKV) {
-                    ok = waitw(BAR(pd_free) + 8u * odd, pd_use ^ 1, W);
-                    if (!ok) break;
+                    ok &= waitw(BAR(pd_free) + 8u * odd, pd_use ^ 1, W);
                     tc_fence_after();
                 }
                 store_half(tmem + lane_base + T::ds(odd, 0), v);
@@ -545,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(BAR(ds_full) + 8u * odd);
+                warp_arrive(BAR(ds_full) + 8u * odd, lane);
                 // the next but one step's buffers and phases
                 pd_use ^= 1;
                 if (NBUF == 2) {
@@ -607,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x.steps > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(BAR(out_free));
+                warp_arrive(BAR(out_free), lane);
             }
         }
     }

@@ -412,8 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < kBN / 32; ++h) tmem_ld32(tmem + lane_base + sb_col + h * 32, s + h * 32);
                 tmem_wait_ld();
-                if (!win_all(first_row, last_row, j0, j0 + kBN)) {
-                    asm volatile("" ::: "memory");   // a branch, not 64 selects on every tile
+                if (__builtin_expect(!win_all(first_row, last_row, j0, j0 + kBN), 0)) {
                     // bit j: whether the row sees key j0 + j
                     auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
                     const unsigned long long vis = below(lim.s - j0) | (below(lim.hi - j0) & ~below(lim.lo - j0));
@@ -435,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the maximum that O and l are scaled by follows the row's only when it lags by
                 // more than 8 (P <= 2^8, sums in fp32); -inf until the row has seen a key
                 const bool need = mt > m_run + 8.f;
-                if (n > 0 && __any_sync(0xffffffffu, need)) {
+                if (__builtin_expect(n > 0 && __any_sync(0xffffffffu, need), 0)) {
                     ok = waitw(BAR(o_done) + 8u * (kMaxSB * (q) + ((n - 1) % NSB)), pv_parity(n - 1), W);
                     if (!ok) break;
                     tc_fence_after();
@@ -474,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(BAR(p_full) + 8u * (kMaxSB * (q) + (b)));
+                warp_arrive(BAR(p_full) + 8u * (kMaxSB * (q) + (b)), lane);
                 ++n;
             }
             if (!ok) break;
@@ -525,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(BAR(o_free) + 8u * (q));
+                warp_arrive(BAR(o_free) + 8u * (q), lane);
             }
         }
     }
