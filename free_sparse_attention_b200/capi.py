@@ -402,59 +402,65 @@ def attention_layer(p, sched: Schedule, Q, K, V, q_init_idx=None, k_init_idx=Non
     return O
 
 
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the handle of a device's current stream (torch's own shortcut costs a tenth of building a
+# Stream object for it, where this torch has it)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
 def _tensors(fn, p, layouts, named):
     """The layouts argument of a strided call (None when every tensor is dense), after a check
     of each (name, tensor, shape): device, type, shape and contiguous channels."""
     dt = torch.bfloat16 if p.dtype == SCOPE_BF16 else torch.float32
-    dev, lay = named[0][1].device, None
+    index, lay = named[0][1].get_device(), None
     for name, t, shape in named:
-        if t.shape != shape or t.dtype != dt or t.device != dev or not t.is_cuda:
-            raise ValueError(f"{fn}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, wanted {shape} {dt} on {dev}")
+        if t.shape != shape or t.dtype is not dt or t.get_device() != index or index < 0:
+            raise ValueError(f"{fn}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, wanted {shape} {dt} on "
+                             f"{named[0][1].device if index >= 0 else 'a GPU'}")
         if not t.is_contiguous():
             st = t.stride()
             if st[3] != 1:
                 raise ValueError(f"{fn}: the channels of {name} are not contiguous (strides {st})")
             lay = layouts() if lay is None else lay
             setattr(lay, name, Strides(st[0], st[1], st[2]))
-    return lay
+    return None if lay is None else ctypes.byref(lay)
 
 
-def _vector(fn, name, t, n, dtype, dev):
-    if t is not None and (t.shape != (n,) or t.dtype != dtype or t.device != dev or not t.is_contiguous()):
-        raise ValueError(f"{fn}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, wanted ({n},) {dtype} on {dev}")
-    return None if t is None else t.data_ptr()
+def _vector(fn, name, t, n, dtype, index):
+    if t is None:
+        return None
+    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, wanted ({n},) {dtype} on the "
+                         f"tensors' device {index}")
+    return t.data_ptr()
 
 
-def _workspace(fn, ws, dev):
-    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"{fn}: the workspace is not a contiguous uint8 tensor on {dev}")
+def _workspace(fn, ws, index):
+    if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"{fn}: the workspace is not a contiguous uint8 tensor on the tensors' device {index}")
 
 
-class _On:
-    """The tensors' device as the current one, and the stream of the call on it; memory that
-    the call allocated is kept for a stream other than the current one."""
+def _new(t, shape):
+    """An output of this shape, dense, like t."""
+    return torch.empty_like(t) if t.shape == shape and t.is_contiguous() else t.new_empty(shape)
 
-    def __init__(self, dev, stream):
-        self.dev, self.stream = dev, stream
 
-    def __enter__(self):
-        self.guard = None
-        if self.dev.index is not None and self.dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return self
+def _on_stream(stream, index, made):
+    """The stream's handle; memory that the call allocated is kept for a stream of the caller's."""
+    if stream is None:
+        return _raw_stream(index)
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
 
-    def handle(self, made):
-        if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
-        for t in made:
-            if t is not None:
-                t.record_stream(self.stream)
-        return self.stream.cuda_stream
+def _elsewhere(t):
+    """Whether t lies on a GPU other than the current one (the call then moves there)."""
+    return t.is_cuda and t.get_device() != torch.cuda.current_device()
 
 
 def alloc_qk_norm_workspace(p, device="cuda") -> torch.Tensor:
@@ -469,47 +475,54 @@ def qk_norm_rope3d(p, Q, K, w_q=None, w_k=None, first=None, out_q=None, out_k=No
     [B,Hkv,N,d] (K may be None) in one pass.  Strided tensors are taken as they are; out_q /
     out_k may be Q / K.  first: int32 [B] positions of the entries' first tokens (default
     p.first).  Returns (Yq, Yk)."""
-    fn, dev = "scope_qk_norm_rope3d", Q.device
-    with _On(dev, stream) as on:
-        Yq = torch.empty((p.B, p.H, p.N, p.d), dtype=Q.dtype, device=dev) if out_q is None else out_q
-        named = [("q", Q, (p.B, p.H, p.N, p.d)), ("yq", Yq, (p.B, p.H, p.N, p.d))]
-        Yk = out_k
-        if K is not None:
-            Yk = torch.empty((p.B, p.Hkv, p.N, p.d), dtype=K.dtype, device=dev) if out_k is None else out_k
-            named += [("k", K, (p.B, p.Hkv, p.N, p.d)), ("yk", Yk, (p.B, p.Hkv, p.N, p.d))]
-        lay = _tensors(fn, p, QkNormLayouts, named)
-        wq, wk = (_vector(fn, n, t, p.d, torch.float32, dev) for n, t in (("w_q", w_q), ("w_k", w_k)))
-        _check(fn, lib().scope_qk_norm_rope3d(
-            ctypes.byref(p), None if lay is None else ctypes.byref(lay), Q.data_ptr(),
-            None if K is None else K.data_ptr(), wq, wk, _vector(fn, "first", first, p.B, torch.int32, dev),
-            Yq.data_ptr(), None if Yk is None else Yk.data_ptr(), on.handle((Yq, Yk))))
+    if _elsewhere(Q):
+        with torch.cuda.device(Q.device):
+            return qk_norm_rope3d(p, Q, K, w_q, w_k, first, out_q, out_k, stream)
+    fn, index, qs = "scope_qk_norm_rope3d", Q.get_device(), (p.B, p.H, p.N, p.d)
+    Yq = _new(Q, qs) if out_q is None else out_q
+    if K is None:
+        Yk = kp = yp = None
+        lay = _tensors(fn, p, QkNormLayouts, (("q", Q, qs), ("yq", Yq, qs)))
+    else:
+        ks = (p.B, p.Hkv, p.N, p.d)
+        Yk = _new(K, ks) if out_k is None else out_k
+        lay = _tensors(fn, p, QkNormLayouts, (("q", Q, qs), ("yq", Yq, qs), ("k", K, ks), ("yk", Yk, ks)))
+        kp, yp = K.data_ptr(), Yk.data_ptr()
+    _check(fn, lib().scope_qk_norm_rope3d(
+        ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, index),
+        _vector(fn, "w_k", w_k, p.d, torch.float32, index), _vector(fn, "first", first, p.B, torch.int32, index),
+        Yq.data_ptr(), yp, _on_stream(stream, index, (Yq, Yk))))
     return Yq, Yk
 
 
 def qk_norm_rope3d_backward(p, Q, K, w_q, w_k, dYq, dYk, first=None, ws=None, out_q=None, out_k=None, stream=None):
     """Gradients of qk_norm_rope3d: (dQ, dK, dw_q, dw_k), dw float32 [d].  K and dYk may be
     None (their gradients then are); out_q / out_k may be dYq / dYk."""
-    fn, dev = "scope_qk_norm_rope3d_backward", Q.device
-    with _On(dev, stream) as on:
-        ws = alloc_qk_norm_workspace(p, dev) if ws is None else ws
-        _workspace(fn, ws, dev)
-        dQ = torch.empty((p.B, p.H, p.N, p.d), dtype=Q.dtype, device=dev) if out_q is None else out_q
-        dw = torch.empty((2, p.d), dtype=torch.float32, device=dev)
-        dwq, dwk = dw[0], None
-        named = [(n, t, (p.B, p.H, p.N, p.d)) for n, t in (("q", Q), ("yq", dYq), ("dq", dQ))]
-        dK = out_k
-        if K is not None:
-            dK = torch.empty((p.B, p.Hkv, p.N, p.d), dtype=K.dtype, device=dev) if out_k is None else out_k
-            dwk = dw[1]
-            named += [(n, t, (p.B, p.Hkv, p.N, p.d)) for n, t in (("k", K), ("yk", dYk), ("dk", dK))]
-        lay = _tensors(fn, p, QkNormLayouts, named)
-        wq, wk = (_vector(fn, n, t, p.d, torch.float32, dev) for n, t in (("w_q", w_q), ("w_k", w_k)))
-        _check(fn, lib().scope_qk_norm_rope3d_backward(
-            ctypes.byref(p), None if lay is None else ctypes.byref(lay), Q.data_ptr(),
-            None if K is None else K.data_ptr(), wq, wk, dYq.data_ptr(), None if dYk is None else dYk.data_ptr(),
-            _vector(fn, "first", first, p.B, torch.int32, dev), dQ.data_ptr(), None if dK is None else dK.data_ptr(),
-            dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), ws.data_ptr(), ws.numel(),
-            on.handle((ws, dQ, dK, dw))))
+    if _elsewhere(Q):
+        with torch.cuda.device(Q.device):
+            return qk_norm_rope3d_backward(p, Q, K, w_q, w_k, dYq, dYk, first, ws, out_q, out_k, stream)
+    fn, index, qs = "scope_qk_norm_rope3d_backward", Q.get_device(), (p.B, p.H, p.N, p.d)
+    if (K is None) != (dYk is None):
+        raise ValueError(f"{fn}: K and dYk go together")
+    ws = alloc_qk_norm_workspace(p, Q.device) if ws is None else ws
+    _workspace(fn, ws, index)
+    dQ = _new(Q, qs) if out_q is None else out_q
+    dw = Q.new_empty((2, p.d), dtype=torch.float32)
+    dwq = dw[0]
+    if K is None:
+        dK = dwk = kp = gp = dp = wp = None
+        lay = _tensors(fn, p, QkNormLayouts, (("q", Q, qs), ("yq", dYq, qs), ("dq", dQ, qs)))
+    else:
+        ks = (p.B, p.Hkv, p.N, p.d)
+        dK, dwk = _new(K, ks) if out_k is None else out_k, dw[1]
+        lay = _tensors(fn, p, QkNormLayouts, (("q", Q, qs), ("yq", dYq, qs), ("dq", dQ, qs), ("k", K, ks),
+                                              ("yk", dYk, ks), ("dk", dK, ks)))
+        kp, gp, dp, wp = K.data_ptr(), dYk.data_ptr(), dK.data_ptr(), dwk.data_ptr()
+    _check(fn, lib().scope_qk_norm_rope3d_backward(
+        ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, index),
+        _vector(fn, "w_k", w_k, p.d, torch.float32, index), dYq.data_ptr(), gp,
+        _vector(fn, "first", first, p.B, torch.int32, index), dQ.data_ptr(), dp, dwq.data_ptr(), wp, ws.data_ptr(),
+        ws.numel(), _on_stream(stream, index, (ws, dQ, dK, dw))))
     return dQ, dK, dwq, dwk
 
 
@@ -525,43 +538,44 @@ def window_attention(p, Q, K, V, q_first=None, k_len=None, ws=None, out=None, ls
     frames, and the first p.sinks frames.  q_first, k_len: int32 [B] position of each entry's
     first query and its number of keys (default p.q_first and Nk).  Returns O, or (O, lse
     [B,H,Nq] float32) with lse=True, which window_attention_backward needs."""
-    fn, dev = "scope_window_attention", Q.device
-    with _On(dev, stream) as on:
-        ws = alloc_window_workspace(p, dev) if ws is None else ws
-        _workspace(fn, ws, dev)
-        O = torch.empty((p.B, p.H, p.Nq, p.d), dtype=Q.dtype, device=dev) if out is None else out
-        L = torch.empty((p.B, p.H, p.Nq), dtype=torch.float32, device=dev) if lse else None
-        qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
-        lay = _tensors(fn, p, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", O, qs)))
-        _check(fn, lib().scope_window_attention(
-            ctypes.byref(p), None if lay is None else ctypes.byref(lay), Q.data_ptr(), K.data_ptr(), V.data_ptr(),
-            _vector(fn, "q_first", q_first, p.B, torch.int32, dev), _vector(fn, "k_len", k_len, p.B, torch.int32, dev),
-            O.data_ptr(), None if L is None else L.data_ptr(), ws.data_ptr(), ws.numel(), on.handle((ws, O, L))))
+    if _elsewhere(Q):
+        with torch.cuda.device(Q.device):
+            return window_attention(p, Q, K, V, q_first, k_len, ws, out, lse, stream)
+    fn, index = "scope_window_attention", Q.get_device()
+    qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
+    ws = alloc_window_workspace(p, Q.device) if ws is None else ws
+    _workspace(fn, ws, index)
+    O = _new(Q, qs) if out is None else out
+    L = Q.new_empty(qs[:3], dtype=torch.float32) if lse else None
+    lay = _tensors(fn, p, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", O, qs)))
+    _check(fn, lib().scope_window_attention(
+        ctypes.byref(p), lay, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+        _vector(fn, "q_first", q_first, p.B, torch.int32, index), _vector(fn, "k_len", k_len, p.B, torch.int32, index),
+        O.data_ptr(), None if L is None else L.data_ptr(), ws.data_ptr(), ws.numel(),
+        _on_stream(stream, index, (ws, O, L))))
     return (O, L) if lse else O
 
 
 def window_attention_backward(p, Q, K, V, O, dO, lse, q_first=None, k_len=None, ws=None, out=None, stream=None):
     """Gradients (dQ, dK, dV) of window_attention from its inputs, O and lse, and dO.  out: a
     triple of tensors to write them to (strided ones too, e.g. the slices of one buffer)."""
-    fn, dev = "scope_window_attention_backward", Q.device
-    with _On(dev, stream) as on:
-        ws = alloc_window_workspace(p, dev) if ws is None else ws
-        _workspace(fn, ws, dev)
-        qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
-        if out is None:
-            dQ = torch.empty(qs, dtype=Q.dtype, device=dev)
-            dK, dV = torch.empty(ks, dtype=Q.dtype, device=dev), torch.empty(ks, dtype=Q.dtype, device=dev)
-        else:
-            dQ, dK, dV = out
-        if lse.shape != qs[:3] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
-            raise ValueError(f"{fn}: lse is not a contiguous float32 tensor {qs[:3]} on {dev}")
-        lay = _tensors(fn, p, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", O, qs), ("d_o", dO, qs),
-                                              ("dq", dQ, qs), ("dk", dK, ks), ("dv", dV, ks)))
-        _check(fn, lib().scope_window_attention_backward(
-            ctypes.byref(p), None if lay is None else ctypes.byref(lay), Q.data_ptr(), K.data_ptr(), V.data_ptr(),
-            O.data_ptr(), dO.data_ptr(), lse.data_ptr(), _vector(fn, "q_first", q_first, p.B, torch.int32, dev),
-            _vector(fn, "k_len", k_len, p.B, torch.int32, dev), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),
-            ws.data_ptr(), ws.numel(), on.handle((ws, dQ, dK, dV))))
+    if _elsewhere(Q):
+        with torch.cuda.device(Q.device):
+            return window_attention_backward(p, Q, K, V, O, dO, lse, q_first, k_len, ws, out, stream)
+    fn, index = "scope_window_attention_backward", Q.get_device()
+    qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
+    ws = alloc_window_workspace(p, Q.device) if ws is None else ws
+    _workspace(fn, ws, index)
+    dQ, dK, dV = (_new(Q, qs), _new(K, ks), _new(V, ks)) if out is None else out
+    if lse.shape != qs[:3] or lse.dtype is not torch.float32 or lse.get_device() != index or not lse.is_contiguous():
+        raise ValueError(f"{fn}: lse is not a contiguous float32 tensor {qs[:3]} on the tensors' device {index}")
+    lay = _tensors(fn, p, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", O, qs), ("d_o", dO, qs),
+                                          ("dq", dQ, qs), ("dk", dK, ks), ("dv", dV, ks)))
+    _check(fn, lib().scope_window_attention_backward(
+        ctypes.byref(p), lay, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), lse.data_ptr(),
+        _vector(fn, "q_first", q_first, p.B, torch.int32, index), _vector(fn, "k_len", k_len, p.B, torch.int32, index),
+        dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), ws.numel(),
+        _on_stream(stream, index, (ws, dQ, dK, dV))))
     return dQ, dK, dV
 
 

@@ -117,9 +117,10 @@ scope_status norm_args(const scope_qk_norm_params &p, const int32_t *first, Norm
     a.first0 = p.first;
     a.eps = (float)p.eps;
     const int ranges[3] = {p.d_t, p.d_h, p.d_w};
+    const double lb = std::log2(p.base);
     int k = 0;
     for (int w : ranges)
-        for (int i = 0; i < w / 2; ++i) a.freq[k++] = std::pow(p.base, -2.0 * i / w) / (2.0 * 3.14159265358979323846);
+        for (int i = 0; i < w / 2; ++i) a.freq[k++] = std::exp2(-2.0 * i / w * lb) * 0.15915494309189535;   // / 2 pi
     return SCOPE_OK;
 }
 

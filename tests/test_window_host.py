@@ -133,8 +133,22 @@ def test_binding_refuses_tensors_that_do_not_fit():
         with pytest.raises(ValueError):
             capi._tensors("f", p, capi.WindowLayouts, (("q", args[0], (2, 4, 30, 64)), ("k", args[1], (2, 2, 40, 64))))
     with pytest.raises(ValueError):
-        capi._vector("f", "k_len", torch.zeros(3, dtype=torch.int32), 2, torch.int32, torch.device("cpu"))
+        capi._vector("f", "k_len", torch.zeros(3, dtype=torch.int32), 2, torch.int32, -1)
     with pytest.raises(ValueError):
-        capi._vector("f", "k_len", torch.zeros(2, dtype=torch.int64), 2, torch.int32, torch.device("cpu"))
+        capi._vector("f", "k_len", torch.zeros(2, dtype=torch.int64), 2, torch.int32, -1)
     with pytest.raises(ValueError):
-        capi._workspace("f", torch.zeros(4, dtype=torch.float32), torch.device("cpu"))
+        capi._workspace("f", torch.zeros(4, dtype=torch.float32), -1)
+
+
+def test_binding_refuses_calls_off_the_gpu():
+    p, q = _window(dtype=0), _norm(dtype=0)
+    Q, K = torch.zeros((2, 4, 30, 64)), torch.zeros((2, 2, 40, 64))
+    ws = torch.empty(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        capi.window_attention(p, Q, K, K, ws=ws)
+    with pytest.raises(ValueError):
+        capi.window_attention_backward(p, Q, K, K, Q, Q, torch.zeros((2, 4, 30)), ws=ws)
+    with pytest.raises(ValueError):
+        capi.qk_norm_rope3d(q, Q, K[:, :, :30])
+    with pytest.raises(ValueError):
+        capi.qk_norm_rope3d_backward(q, Q, None, None, None, Q, Q, ws=ws)
