@@ -20,12 +20,12 @@ struct NormArgs {
     int first0;
     float eps;
     double freq[64];     // turns per position of channel pair i
-    float *partial;      // [2, blocks, d] weight-gradient partials (backward)
+    float *partial;      // [blocks, d] weight-gradient partials (backward)
     int32_t *status;     // cleared by the backward kernel
-    int tiles, chunk, chunks_q, chunks_k;   // filled by the launchers
+    int tiles, chunk, chunks_q, chunks_k, blocks_q;   // filled by the launchers
 };
 
-constexpr int kNormMaxBlocks = 148 * 4;   // blocks of the backward pass (partials in the workspace)
+constexpr int kNormMaxBlocks = 148 * 4;   // most blocks of the backward pass (partials in the workspace)
 
 __device__ __forceinline__ int norm_first(const NormArgs &a, int b)
 {
