@@ -164,8 +164,8 @@ Plan plan_of(const scope_window_params &p)
     // rows of one item and keys of one of its tiles: few rows, tensor cores, or fp32; items
     // that the device holds at a time
     const bool bf16 = p.dtype == SCOPE_BF16;
-    const int bm = r.few ? 16 : (bf16 ? 256 : 64), bn = r.few && bf16 ? 16 : 64;
-    const int slots = kPlanSms * (bf16 ? (r.few ? 2 : 1) : (r.few ? 3 : 1));
+    const int bm = r.few ? 16 : (bf16 ? 256 : 32), bn = r.few && bf16 ? 16 : 64;
+    const int slots = kPlanSms * (bf16 ? (r.few ? 2 : 1) : (p.d == 64 ? 4 : 2));
     const long long rows = (long long)r.pack * p.Nq, tiles = (rows + bm - 1) / bm;
     const long long items = (long long)p.B * (p.H / r.pack) * tiles;
     // key tiles of one item, at most

@@ -4,19 +4,25 @@
 //   with D_i = dO_i . O_i:  dV_j = sum_i p_ij dO_i,  ds_ij = p_ij (dO_i . v_j - D_i) / sqrt d,
 //   dQ_i = sum_j ds_ij k_j,  dK_j = sum_i ds_ij q_i.
 //
-// One block holds a tile of rows against tiles of 64 columns; both sides lie row-major in
+// A block of 128 threads holds 32 rows against tiles of 64 columns; both sides lie row-major in
 // shared memory with rows padded by 4 floats, so that the 16-byte reads of 16 neighbouring
-// rows meet different banks.  A thread owns rows ty + 16 i and columns tx + 16 j of a
-// score tile (4 x 4 scores from 8 16-byte reads per 4 channels, 64 FMAs), and rows ty + 16 i
-// and channels 4 tx + 64 j .. + 3 of an output.  Scores, softmax statistics and all sums are
-// fp32.  Bound by the FMA pipe (74 TFLOP/s).
+// rows meet different banks.  A thread owns rows ty + 8 i and columns tx + 16 j of a score tile
+// (4 x 4 scores from 8 16-byte reads per 4 channels, 64 FMAs in 32 packed instructions), and rows ty + 8 i and channels
+// 4 tx + 64 j .. + 3 of an output.  Tiles arrive by cp.async as soon as their place is free, and
+// two blocks (four at d = 64) share an SM, so that one computes while the other waits.  Scores,
+// softmax statistics and all sums are fp32.  Bound by the FMA pipe (74 TFLOP/s) and, next to it,
+// by the shared-memory reads that feed it.
 #include "window.cuh"
 
 namespace scope {
 
 namespace {
 
+// threads: 8 (ty) x 16 (tx); a warp holds 2 x 16, neighbouring lanes at the same column, so that a
+// 16-byte read of 16 columns by 32 lanes is two wavefronts and one of 2 rows a single one
+constexpr int kTh = 128;
 constexpr int kBN = 64;      // columns of a score tile
+constexpr int kBM = 32;      // rows of the ordinary form
 constexpr int kLdP = kBN + 4;
 
 __device__ __forceinline__ float4 load4(const float *p)
@@ -29,18 +35,35 @@ __device__ __forceinline__ void store4(float *p, float4 v)
     *reinterpret_cast<float4 *>(p) = v;
 }
 
-// Rows of one tile to shared memory (leading dimension D + 4); src(r) is row r's
-// address or NULL for a row of zeros.
+__device__ __forceinline__ void commit()
+{
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+}
+
+// Waits for all but the last N groups of copies, then for the block.
+template <int N>
+__device__ __forceinline__ void arrived()
+{
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+    __syncthreads();
+}
+
+// Starts the copy of one tile's rows to shared memory (leading dimension D + 4), as one group;
+// src(r) is row r's address or NULL for a row of zeros.  any: a valid address.
 template <int D, int ROWS, typename Src>
-__device__ __forceinline__ void load_tile(float *dst, Src src)
+__device__ __forceinline__ void load_tile(float *dst, const float *any, Src src)
 {
     constexpr int C4 = D / 4;
 #pragma unroll 4
-    for (int e = threadIdx.x; e < ROWS * C4; e += 256) {
+    for (int e = threadIdx.x; e < ROWS * C4; e += kTh) {
         const int r = e / C4, c = (e % C4) * 4;
         const float *p = src(r);
-        store4(dst + r * (D + 4) + c, p ? load4(p + c) : make_float4(0.f, 0.f, 0.f, 0.f));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(dst + r * (D + 4) + c)),
+                     "l"(p ? p + c : any), "r"(p ? 16 : 0)
+                     : "memory");
     }
+    commit();
 }
 
 __device__ __forceinline__ void dot4(float &acc, float4 x, float4 y)
@@ -51,67 +74,112 @@ __device__ __forceinline__ void dot4(float &acc, float4 x, float4 y)
     acc = fmaf(x.w, y.w, acc);
 }
 
-// acc[i][j] = rows[ty + 16 i] . cols[tx + 16 j]
+// Two products and sums in one instruction: the blocks are bound by instruction issue before the
+// FMA pipe (96 % against 73 % of the busiest SM's cycles with scalar FMAs).
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t acc)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(acc));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+
+__device__ __forceinline__ float2 unpair(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+
+__device__ __forceinline__ ulonglong2 load22(const float *p)
+{
+    return *reinterpret_cast<const ulonglong2 *>(p);
+}
+
+// acc[i][j] = rows[ty + 8 i] . cols[tx + 16 j]: even and odd channels summed apart.
 template <int D, int MI>
 __device__ __forceinline__ void scores(float (&acc)[MI][4], const float *rows, const float *cols, int ty, int tx)
 {
+    uint64_t s[MI][4];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) s[i][j] = 0ull;
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-        float4 x[MI], y[4];
+        ulonglong2 x[MI], y[4];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) x[i] = *reinterpret_cast<const float4 *>(rows + (ty + 16 * i) * (D + 4) + c);
+        for (int i = 0; i < MI; ++i) x[i] = load22(rows + (ty + 8 * i) * (D + 4) + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(cols + (tx + 16 * j) * (D + 4) + c);
+        for (int j = 0; j < 4; ++j) y[j] = load22(cols + (tx + 16 * j) * (D + 4) + c);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dot4(acc[i][j], x[i], y[j]);
+            for (int j = 0; j < 4; ++j) s[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, s[i][j]));
     }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = unpair(s[i][j]);
+            acc[i][j] = f.x + f.y;
+        }
 }
 
-// out[i][4 jj + e] += sum_k w[ty + 16 i][k] cols[k][4 tx + 64 jj + e]
+// out[i][2 jj], [2 jj + 1] (channels 4 tx + 64 jj .. + 3 in pairs) += sum_k w[ty + 8 i][k] cols[k][...]
 template <int D, int MI>
-__device__ __forceinline__ void accumulate(float (&out)[MI][D / 16], const float *w, const float *cols, int ty, int tx)
+__device__ __forceinline__ void accumulate(uint64_t (&out)[MI][D / 32], const float *w, const float *cols, int ty, int tx)
 {
 #pragma unroll 2
     for (int k = 0; k < kBN; k += 4) {
         float4 p[MI];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) p[i] = *reinterpret_cast<const float4 *>(w + (ty + 16 * i) * kLdP + k);
+        for (int i = 0; i < MI; ++i) p[i] = load4(w + (ty + 8 * i) * kLdP + k);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
+            uint64_t pk[MI];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const float v = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                pk[i] = pair(v, v);
+            }
 #pragma unroll
             for (int jj = 0; jj < D / 64; ++jj) {
-                const float4 v = *reinterpret_cast<const float4 *>(cols + (k + kk) * (D + 4) + 4 * tx + 64 * jj);
+                const ulonglong2 v = load22(cols + (k + kk) * (D + 4) + 4 * tx + 64 * jj);
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
-                    const float pk = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-                    out[i][4 * jj + 0] = fmaf(pk, v.x, out[i][4 * jj + 0]);
-                    out[i][4 * jj + 1] = fmaf(pk, v.y, out[i][4 * jj + 1]);
-                    out[i][4 * jj + 2] = fmaf(pk, v.z, out[i][4 * jj + 2]);
-                    out[i][4 * jj + 3] = fmaf(pk, v.w, out[i][4 * jj + 3]);
+                    out[i][2 * jj] = fma2(pk[i], v.x, out[i][2 * jj]);
+                    out[i][2 * jj + 1] = fma2(pk[i], v.y, out[i][2 * jj + 1]);
                 }
             }
         }
     }
 }
 
-// Forward: BM rows of one unit (b, group of a.pack query heads) against one share of the key
-// tiles they see.  16 x 16 threads (BM = 64, 4 rows each) or 16 x 16 with one row each (BM =
-// 16, the form for few rows, which would leave most of a 64-row tile idle).
-template <int D, int BM>
-__global__ void __launch_bounds__(256) window_fwd_kernel(WinArgs a)
+// 4 channels 4 tx + 64 jj .. + 3 of one row, scaled.
+__device__ __forceinline__ void store_scaled(float *p, const uint64_t *v, float scale)
 {
-    constexpr int MI = BM / 16;
+    const float2 x = unpair(v[0]), y = unpair(v[1]);
+    store4(p, make_float4(x.x * scale, x.y * scale, y.x * scale, y.y * scale));
+}
+
+// Forward: BM rows of one unit (b, group of a.pack query heads) against one share of the key
+// tiles they see.  BM = 32, or 16 (two rows per thread) where a unit's rows fill no more.
+template <int D, int BM>
+__global__ void __launch_bounds__(kTh) window_fwd_kernel(WinArgs a)
+{
+    constexpr int MI = BM / 8;
     extern __shared__ __align__(16) float sm[];
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;   // this path has no device conditions
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float *sq = sm, *sk = sq + BM * (D + 4), *sv = sk + kBN * (D + 4), *sp = sv + kBN * (D + 4);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
     const int rows = a.pack * a.Nq, tiles = (rows + BM - 1) / BM;
     // item = ((unit * tiles) + tile) * splits + split
     long long it = blockIdx.x;
@@ -128,46 +196,56 @@ __global__ void __launch_bounds__(256) window_fwd_kernel(WinArgs a)
     const WinRow ra = win_row(a, first + ia, kl), rz = win_row(a, first + iz, kl);
     const WinTiles wt = win_tiles<kBN>(ra, rz);
     const int nt = wt.count(), t0 = (int)((long long)nt * split / a.splits), t1 = (int)((long long)nt * (split + 1) / a.splits);
-
-    load_tile<D, BM>(sq, [&](int r) -> const float * {
+    const float *qb = static_cast<const float *>(a.Q) + b * a.lq.b;
+    const float *kb = static_cast<const float *>(a.K) + b * a.lk.b + hk * a.lk.h;
+    const float *vb = static_cast<const float *>(a.V) + b * a.lv.b + hk * a.lv.h;
+    // a key tile of K or V; rows that no row of the tile sees are not read (they may hold anything)
+    auto keys = [&](float *dst, const float *base, long long stride, int t) {
+        if (t >= t1) return commit();
+        const int j0 = wt.at(t) * kBN;
+        load_tile<D, kBN>(dst, base, [&](int r) -> const float * {
+            const int j = j0 + r;
+            return j < ra.s || (j >= ra.lo && j < rz.hi) ? base + j * stride : nullptr;
+        });
+    };
+    load_tile<D, BM>(sq, qb, [&](int r) -> const float * {
         const int rr = r0 + r;
-        return rr < r1 ? static_cast<const float *>(a.Q) + b * a.lq.b + (h0 + rr / a.Nq) * a.lq.h + (rr % a.Nq) * a.lq.n : nullptr;
+        return rr < r1 ? qb + (h0 + rr / a.Nq) * a.lq.h + (rr % a.Nq) * a.lq.n : nullptr;
     });
+    keys(sk, kb, a.lk.n, t0);
+    keys(sv, vb, a.lv.n, t0);
     WinRow lim[MI];
-    float m[MI], l[MI], o[MI][D / 16];
+    float m[MI], l[MI];
+    uint64_t o[MI][D / 32];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const int rr = r0 + ty + 16 * i;
+        const int rr = r0 + ty + 8 * i;
         lim[i] = rr < r1 ? win_row(a, first + rr % a.Nq, kl) : WinRow{0, 0, 0};
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) o[i][e] = 0.f;
+        for (int e = 0; e < D / 32; ++e) o[i][e] = 0ull;
     }
-    const float *kb = static_cast<const float *>(a.K) + b * a.lk.b + hk * a.lk.h;
-    const float *vb = static_cast<const float *>(a.V) + b * a.lv.b + hk * a.lv.h;
     for (int t = t0; t < t1; ++t) {
         const int j0 = wt.at(t) * kBN;
-        __syncthreads();
-        // keys and values that no row of the tile sees are not read (they may hold anything)
-        auto seen = [&](int j) { return j < ra.s || (j >= ra.lo && j < rz.hi); };
-        load_tile<D, kBN>(sk, [&](int r) { return seen(j0 + r) ? kb + (j0 + r) * a.lk.n : nullptr; });
-        load_tile<D, kBN>(sv, [&](int r) { return seen(j0 + r) ? vb + (j0 + r) * a.lv.n : nullptr; });
-        __syncthreads();
+        arrived<1>();
         float s[MI][4];
         scores<D, MI>(s, sq, sk, ty, tx);
+        __syncthreads();
+        keys(sk, kb, a.lk.n, t + 1);
+        const bool all = win_all(ra, rz, j0, j0 + kBN);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             float mt = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int key = j0 + tx + 16 * j;
-                const bool vis = key < lim[i].s || (key >= lim[i].lo && key < lim[i].hi);
+                const bool vis = all || key < lim[i].s || (key >= lim[i].lo && key < lim[i].hi);
                 s[i][j] = vis ? s[i][j] * a.scale_log2 : -INFINITY;
                 mt = fmaxf(mt, s[i][j]);
             }
 #pragma unroll
-            for (int x = 8; x; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+            for (int x = 16; x > 1; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
             const float mn = fmaxf(m[i], mt), base = mn == -INFINITY ? 0.f : mn;
             const float corr = exp2f(m[i] - base);
             float ls = 0.f;
@@ -175,40 +253,38 @@ __global__ void __launch_bounds__(256) window_fwd_kernel(WinArgs a)
             for (int j = 0; j < 4; ++j) {
                 s[i][j] = exp2f(s[i][j] - base);
                 ls += s[i][j];
-                sp[(ty + 16 * i) * kLdP + tx + 16 * j] = s[i][j];
+                sp[(ty + 8 * i) * kLdP + tx + 16 * j] = s[i][j];
             }
-#pragma unroll
-            for (int x = 8; x; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-            l[i] = l[i] * corr + ls;
+            l[i] = l[i] * corr + ls;   // of this thread's columns; joined at the end
             m[i] = mn;
+            const uint64_t c2 = pair(corr, corr);
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) o[i][e] *= corr;
+            for (int e = 0; e < D / 32; ++e) o[i][e] = fma2(o[i][e], c2, 0ull);
         }
-        __syncwarp();   // a row of sp is written and read by one half warp
+        arrived<1>();
         accumulate<D, MI>(o, sp, sv, ty, tx);
+        __syncthreads();
+        keys(sv, vb, a.lv.n, t + 1);
     }
+    arrived<0>();
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const int rr = r0 + ty + 16 * i;
+#pragma unroll
+        for (int x = 16; x > 1; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+        const int rr = r0 + ty + 8 * i;
         if (rr >= r1) continue;
         const int h = h0 + rr / a.Nq, q = rr % a.Nq;
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];   // no visible key: zeros; NaN stays NaN
         const float lse2 = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
         const long long row = win_row_index(a, b, h, q);
-        if (a.splits > 1) {
-            float *dst = a.part_o + (row * a.splits + split) * D;
+        float *dst = a.splits > 1 ? a.part_o + (row * a.splits + split) * D
+                                  : static_cast<float *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n;
 #pragma unroll
-            for (int jj = 0; jj < D / 64; ++jj)
-                store4(dst + 4 * tx + 64 * jj, make_float4(o[i][4 * jj] * inv, o[i][4 * jj + 1] * inv, o[i][4 * jj + 2] * inv,
-                                                           o[i][4 * jj + 3] * inv));
-            if (tx == 0) a.part_lse[row * a.splits + split] = lse2;
-        } else {
-            float *dst = static_cast<float *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n;
-#pragma unroll
-            for (int jj = 0; jj < D / 64; ++jj)
-                store4(dst + 4 * tx + 64 * jj, make_float4(o[i][4 * jj] * inv, o[i][4 * jj + 1] * inv, o[i][4 * jj + 2] * inv,
-                                                           o[i][4 * jj + 3] * inv));
-            if (tx == 0 && a.lse) a.lse[row] = lse2 * 0.6931471805599453f;
+        for (int jj = 0; jj < D / 64; ++jj)
+            store_scaled(dst + 4 * tx + 64 * jj, &o[i][2 * jj], inv);
+        if (tx == 0) {
+            if (a.splits > 1) a.part_lse[row * a.splits + split] = lse2;
+            else if (a.lse) a.lse[row] = lse2 * 0.6931471805599453f;
         }
     }
 }
@@ -251,32 +327,46 @@ __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a)
     if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
-// dQ: 64 query rows of one head against the key tiles they see; also writes D_i.
+// dQ: 32 query rows of one head against the key tiles they see; also writes D_i.
 template <int D>
-__global__ void __launch_bounds__(256) window_dq_kernel(WinArgs a)
+__global__ void __launch_bounds__(kTh) window_dq_kernel(WinArgs a)
 {
-    constexpr int BM = 64, MI = 4;
+    constexpr int MI = kBM / 8;
     extern __shared__ __align__(16) float sm[];
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
-    float *sq = sm, *sg = sq + BM * (D + 4), *sk = sg + BM * (D + 4), *sv = sk + kBN * (D + 4), *sp = sv + kBN * (D + 4);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int tiles = (a.Nq + BM - 1) / BM;
+    float *sq = sm, *sg = sq + kBM * (D + 4), *sk = sg + kBM * (D + 4), *sv = sk + kBN * (D + 4), *sp = sv + kBN * (D + 4);
+    const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
+    const int tiles = (a.Nq + kBM - 1) / kBM;
     const int tile = (int)(blockIdx.x % tiles), bh = (int)(blockIdx.x / tiles);
     const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hkv);
-    const int r0 = tile * BM, r1 = min(a.Nq, r0 + BM);
+    const int r0 = tile * kBM, r1 = min(a.Nq, r0 + kBM);
     const int first = win_first(a, b), kl = win_klen(a, b);
     const WinRow ra = win_row(a, first + r0, kl), rz = win_row(a, first + r1 - 1, kl);
     const WinTiles wt = win_tiles<kBN>(ra, rz);
+    const int nt = wt.count();
     const float *qb = static_cast<const float *>(a.Q) + b * a.lq.b + h * a.lq.h;
     const float *gb = static_cast<const float *>(a.G) + b * a.lg.b + h * a.lg.h;
-    load_tile<D, BM>(sq, [&](int r) { return r0 + r < r1 ? qb + (r0 + r) * a.lq.n : nullptr; });
-    load_tile<D, BM>(sg, [&](int r) { return r0 + r < r1 ? gb + (r0 + r) * a.lg.n : nullptr; });
-    __syncthreads();
+    const float *kb = static_cast<const float *>(a.K) + b * a.lk.b + hk * a.lk.h;
+    const float *vb = static_cast<const float *>(a.V) + b * a.lv.b + hk * a.lv.h;
+    auto keys = [&](float *dst, const float *base, long long stride, int t) {
+        if (t >= nt) return commit();
+        const int j0 = wt.at(t) * kBN;
+        load_tile<D, kBN>(dst, base, [&](int r) -> const float * {
+            const int j = j0 + r;
+            return j < ra.s || (j >= ra.lo && j < rz.hi) ? base + j * stride : nullptr;
+        });
+    };
+    load_tile<D, kBM>(sq, qb, [&](int r) -> const float * { return r0 + r < r1 ? qb + (r0 + r) * a.lq.n : nullptr; });
+    load_tile<D, kBM>(sg, gb, [&](int r) -> const float * { return r0 + r < r1 ? gb + (r0 + r) * a.lg.n : nullptr; });
+    keys(sv, vb, a.lv.n, 0);
+    keys(sk, kb, a.lk.n, 0);
+    arrived<2>();
     WinRow lim[MI];
-    float lse[MI], dl[MI], dq[MI][D / 16];
+    float lse[MI], dl[MI];
+    uint64_t dq[MI][D / 32];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const int q = r0 + ty + 16 * i;
+        const int q = r0 + ty + 8 * i;
         const bool in = q < r1;
         lim[i] = in ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
         const long long row = win_row_index(a, b, h, in ? q : r0);
@@ -287,123 +377,130 @@ __global__ void __launch_bounds__(256) window_dq_kernel(WinArgs a)
 #pragma unroll
             for (int jj = 0; jj < D / 64; ++jj) {
                 const int c = 4 * tx + 64 * jj;
-                dot4(s, load4(ob + c), *reinterpret_cast<const float4 *>(sg + (ty + 16 * i) * (D + 4) + c));
+                dot4(s, load4(ob + c), load4(sg + (ty + 8 * i) * (D + 4) + c));
             }
         }
 #pragma unroll
-        for (int x = 8; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        for (int x = 16; x > 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
         dl[i] = s;
         if (in && tx == 0) a.delta[row] = s;
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) dq[i][e] = 0.f;
+        for (int e = 0; e < D / 32; ++e) dq[i][e] = 0ull;
     }
-    const float *kb = static_cast<const float *>(a.K) + b * a.lk.b + hk * a.lk.h;
-    const float *vb = static_cast<const float *>(a.V) + b * a.lv.b + hk * a.lv.h;
-    for (int t = 0; t < wt.count(); ++t) {
+    for (int t = 0; t < nt; ++t) {
         const int j0 = wt.at(t) * kBN;
-        __syncthreads();
-        auto seen = [&](int j) { return j < ra.s || (j >= ra.lo && j < rz.hi); };
-        load_tile<D, kBN>(sk, [&](int r) { return seen(j0 + r) ? kb + (j0 + r) * a.lk.n : nullptr; });
-        load_tile<D, kBN>(sv, [&](int r) { return seen(j0 + r) ? vb + (j0 + r) * a.lv.n : nullptr; });
-        __syncthreads();
+        arrived<1>();
         float s[MI][4], dp[MI][4];
-        scores<D, MI>(s, sq, sk, ty, tx);
         scores<D, MI>(dp, sg, sv, ty, tx);
+        arrived<0>();
+        keys(sv, vb, a.lv.n, t + 1);
+        scores<D, MI>(s, sq, sk, ty, tx);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int key = j0 + tx + 16 * j;
                 const bool vis = key < lim[i].s || (key >= lim[i].lo && key < lim[i].hi);
-                sp[(ty + 16 * i) * kLdP + tx + 16 * j] =
+                sp[(ty + 8 * i) * kLdP + tx + 16 * j] =
                     vis ? exp2f(fmaf(s[i][j], a.scale_log2, -lse[i])) * (dp[i][j] - dl[i]) : 0.f;
             }
-        __syncwarp();
+        __syncwarp();   // a row of sp is written and read by one warp
         accumulate<D, MI>(dq, sp, sk, ty, tx);
+        __syncthreads();
+        keys(sk, kb, a.lk.n, t + 1);
     }
+    arrived<0>();
     float *dst = static_cast<float *>(a.dQ) + b * a.ldq.b + h * a.ldq.h;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const int q = r0 + ty + 16 * i;
+        const int q = r0 + ty + 8 * i;
         if (q >= r1) continue;
 #pragma unroll
         for (int jj = 0; jj < D / 64; ++jj)
-            store4(dst + q * a.ldq.n + 4 * tx + 64 * jj,
-                   make_float4(dq[i][4 * jj] * a.scale, dq[i][4 * jj + 1] * a.scale, dq[i][4 * jj + 2] * a.scale,
-                               dq[i][4 * jj + 3] * a.scale));
+            store_scaled(dst + q * a.ldq.n + 4 * tx + 64 * jj, &dq[i][2 * jj], a.scale);
     }
 }
 
-// dK, dV: 64 keys of one key head against every query (of all its query heads, in order) that
+// dK, dV: 32 keys of one key head against every query (of all its query heads, in order) that
 // may see one of them.  Scores are taken transposed: rows are keys, columns are queries.
 template <int D>
-__global__ void __launch_bounds__(256) window_dkv_kernel(WinArgs a)
+__global__ void __launch_bounds__(kTh) window_dkv_kernel(WinArgs a)
 {
-    constexpr int BM = 64, MI = 4;
+    constexpr int MI = kBM / 8;
     extern __shared__ __align__(16) float sm[];
-    float *sk = sm, *sv = sk + BM * (D + 4), *sq = sv + BM * (D + 4), *sg = sq + kBN * (D + 4), *sp = sg + kBN * (D + 4),
-          *sd = sp + BM * kLdP;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float *sk = sm, *sv = sk + kBM * (D + 4), *sq = sv + kBM * (D + 4), *sg = sq + kBN * (D + 4), *sp = sg + kBN * (D + 4);
+    const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
     // sink blocks meet every later query: they come first in launch order
     const int units = a.B * a.Hkv;
     const int tile = (int)(blockIdx.x / units), bh = (int)(blockIdx.x % units);
     const int b = bh / a.Hkv, hk = bh - b * a.Hkv, G = a.H / a.Hkv;
-    const int j0 = tile * BM, j1 = min(a.Nk, j0 + BM);
+    const int j0 = tile * kBM, j1 = min(a.Nk, j0 + kBM);
     const int first = win_first(a, b), kl = win_klen(a, b);
     const int2 qr = win_queries(a, first, kl, a.Nq, j0, j1);
+    const int per = (qr.y - qr.x + kBN - 1) / kBN, nt = per * G;   // column tiles: per query head, in all
     const float *kb = static_cast<const float *>(a.K) + b * a.lk.b + hk * a.lk.h;
     const float *vb = static_cast<const float *>(a.V) + b * a.lv.b + hk * a.lv.h;
-    load_tile<D, BM>(sk, [&](int r) { return j0 + r < min(j1, kl) ? kb + (j0 + r) * a.lk.n : nullptr; });
-    load_tile<D, BM>(sv, [&](int r) { return j0 + r < min(j1, kl) ? vb + (j0 + r) * a.lv.n : nullptr; });
-    float dk[MI][D / 16], dv[MI][D / 16];
+    auto queries = [&](float *dst, const void *tensor, const WinLayout &lay, int t) {
+        if (t >= nt) return commit();
+        const float *base = static_cast<const float *>(tensor) + b * lay.b + (hk * G + t / per) * lay.h;
+        const int i0 = qr.x + t % per * kBN;
+        load_tile<D, kBN>(dst, base, [&](int r) -> const float * { return i0 + r < qr.y ? base + (i0 + r) * lay.n : nullptr; });
+    };
+    load_tile<D, kBM>(sk, kb, [&](int r) -> const float * { return j0 + r < min(j1, kl) ? kb + (j0 + r) * a.lk.n : nullptr; });
+    load_tile<D, kBM>(sv, vb, [&](int r) -> const float * { return j0 + r < min(j1, kl) ? vb + (j0 + r) * a.lv.n : nullptr; });
+    queries(sg, a.G, a.lg, 0);
+    queries(sq, a.Q, a.lq, 0);
+    uint64_t dk[MI][D / 32], dv[MI][D / 32];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) dk[i][e] = dv[i][e] = 0.f;
-    for (int g = 0; g < G; ++g) {
-        const int h = hk * G + g;
-        const float *qb = static_cast<const float *>(a.Q) + b * a.lq.b + h * a.lq.h;
-        const float *gb = static_cast<const float *>(a.G) + b * a.lg.b + h * a.lg.h;
-        for (int i0 = qr.x; i0 < qr.y; i0 += kBN) {
-            __syncthreads();
-            load_tile<D, kBN>(sq, [&](int r) { return i0 + r < qr.y ? qb + (i0 + r) * a.lq.n : nullptr; });
-            load_tile<D, kBN>(sg, [&](int r) { return i0 + r < qr.y ? gb + (i0 + r) * a.lg.n : nullptr; });
-            __syncthreads();
-            float s[MI][4], dp[MI][4];
-            scores<D, MI>(s, sk, sq, ty, tx);
-            scores<D, MI>(dp, sv, sg, ty, tx);
+        for (int e = 0; e < D / 32; ++e) dk[i][e] = dv[i][e] = 0ull;
+    for (int t = 0; t < nt; ++t) {
+        const int h = hk * G + t / per, i0 = qr.x + t % per * kBN;
+        arrived<0>();
+        float s[MI][4], dp[MI][4];
+        scores<D, MI>(s, sk, sq, ty, tx);
+        scores<D, MI>(dp, sv, sg, ty, tx);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int q = i0 + tx + 16 * j;
-                const bool in = q < qr.y;
-                const WinRow lim = in ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
-                const long long row = win_row_index(a, b, h, in ? q : 0);
-                const float lse = a.lse[row] * 1.4426950408889634f, dl = a.delta[row];
+        for (int j = 0; j < 4; ++j) {
+            const int q = i0 + tx + 16 * j;
+            const bool in = q < qr.y;
+            const WinRow lim = in ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
+            const long long row = win_row_index(a, b, h, in ? q : 0);
+            const float lse = a.lse[row] * 1.4426950408889634f, dl = a.delta[row];
 #pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    const int key = j0 + ty + 16 * i;
-                    const bool vis = key < lim.s || (key >= lim.lo && key < lim.hi);
-                    const float p = vis ? exp2f(fmaf(s[i][j], a.scale_log2, -lse)) : 0.f;
-                    sp[(ty + 16 * i) * kLdP + tx + 16 * j] = p;
-                    sd[(ty + 16 * i) * kLdP + tx + 16 * j] = vis ? p * (dp[i][j] - dl) : 0.f;
-                }
+            for (int i = 0; i < MI; ++i) {
+                const int key = j0 + ty + 8 * i;
+                const bool vis = key < lim.s || (key >= lim.lo && key < lim.hi);
+                s[i][j] = vis ? exp2f(fmaf(s[i][j], a.scale_log2, -lse)) : 0.f;
+                dp[i][j] = vis ? s[i][j] * (dp[i][j] - dl) : 0.f;
+                sp[(ty + 8 * i) * kLdP + tx + 16 * j] = s[i][j];
             }
-            __syncwarp();
-            accumulate<D, MI>(dv, sp, sg, ty, tx);
-            accumulate<D, MI>(dk, sd, sq, ty, tx);
         }
+        __syncwarp();
+        accumulate<D, MI>(dv, sp, sg, ty, tx);
+        __syncthreads();
+        queries(sg, a.G, a.lg, t + 1);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sp[(ty + 8 * i) * kLdP + tx + 16 * j] = dp[i][j];
+        __syncwarp();
+        accumulate<D, MI>(dk, sp, sq, ty, tx);
+        __syncthreads();
+        queries(sq, a.Q, a.lq, t + 1);
     }
+    arrived<0>();
     float *dkb = static_cast<float *>(a.dK) + b * a.ldk.b + hk * a.ldk.h, *dvb = static_cast<float *>(a.dV) + b * a.ldv.b + hk * a.ldv.h;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const int j = j0 + ty + 16 * i;
+        const int j = j0 + ty + 8 * i;
         if (j >= j1) continue;
 #pragma unroll
         for (int jj = 0; jj < D / 64; ++jj) {
             const int c = 4 * tx + 64 * jj;
-            store4(dkb + j * a.ldk.n + c, make_float4(dk[i][4 * jj] * a.scale, dk[i][4 * jj + 1] * a.scale,
-                                                      dk[i][4 * jj + 2] * a.scale, dk[i][4 * jj + 3] * a.scale));
-            store4(dvb + j * a.ldv.n + c, make_float4(dv[i][4 * jj], dv[i][4 * jj + 1], dv[i][4 * jj + 2], dv[i][4 * jj + 3]));
+            store_scaled(dkb + j * a.ldk.n + c, &dk[i][2 * jj], a.scale);
+            store_scaled(dvb + j * a.ldv.n + c, &dv[i][2 * jj], 1.f);
         }
     }
 }
@@ -414,29 +511,28 @@ cudaError_t launch(F *kernel, long long grid, int smem, const WinArgs &a, cudaSt
     if (grid < 1 || grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)grid, 256, smem, s>>>(a);
+    kernel<<<(unsigned)grid, kTh, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t forward(const WinArgs &a, cudaStream_t s)
 {
-    // 16-row tiles when a unit's rows fill at most one of them, 64-row tiles otherwise
+    // 16-row tiles when a unit's rows fill no more than one
     const long long rows = (long long)a.pack * a.Nq, units = (long long)a.B * (a.H / a.pack);
     if (rows <= 16)
         return launch(window_fwd_kernel<D, 16>, units * a.splits, (16 + 2 * kBN) * (D + 4) * 4 + 16 * kLdP * 4, a, s);
-    return launch(window_fwd_kernel<D, 64>, units * ((rows + 63) / 64) * a.splits,
-                  (64 + 2 * kBN) * (D + 4) * 4 + 64 * kLdP * 4, a, s);
+    return launch(window_fwd_kernel<D, kBM>, units * ((rows + kBM - 1) / kBM) * a.splits,
+                  (kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s);
 }
 
 template <int D>
 cudaError_t backward(const WinArgs &a, cudaStream_t s)
 {
-    cudaError_t e = launch(window_dq_kernel<D>, (long long)a.B * a.H * ((a.Nq + 63) / 64),
-                           4 * 64 * (D + 4) * 4 + 64 * kLdP * 4, a, s);
+    const int smem = (2 * kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4;
+    cudaError_t e = launch(window_dq_kernel<D>, (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM), smem, a, s);
     if (e != cudaSuccess) return e;
-    return launch(window_dkv_kernel<D>, (long long)a.B * a.Hkv * ((a.Nk + 63) / 64),
-                  4 * 64 * (D + 4) * 4 + 2 * 64 * kLdP * 4, a, s);
+    return launch(window_dkv_kernel<D>, (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM), smem, a, s);
 }
 
 }  // namespace
