@@ -33,7 +33,7 @@ constexpr int kMaxStages = 8, kMaxBuf = 3, kRing = 4;
 constexpr uint32_t kTmemCols = 512;
 
 struct __align__(8) Bars {
-    uint64_t r_full, r_empty, land, out_full, out_free;
+    uint64_t r_full, r_empty, land, out_full, out_free, sums_full, sums_free;
     uint64_t c_full[kMaxStages], c_empty[kMaxStages], ls_full[kMaxStages];
     uint64_t s_full[kMaxBuf], d_full[kMaxBuf], s_free[kMaxBuf], d_free[kMaxBuf];   // S and dP buffers
     uint64_t p_full[2], ds_full[2], pd_free[2], drain[3];                          // P and dS buffers
@@ -67,7 +67,8 @@ struct Smem {
     static constexpr int kRows = kBM * D * 2, kTile = kBN * D * 2;
     static constexpr int kR1 = 0, kR2 = kRows, kC = 2 * kRows;               // stage s: C1, C2
     static constexpr int kLs = kC + kStages * 2 * kTile;                     // stage s: lse [64], D [64]
-    static constexpr int kBars = kLs + (DKV ? kStages * 2 * kBN * 4 : 0);
+    static constexpr int kSums = kLs;                                        // dQ: [2][128] row sums of dS
+    static constexpr int kBars = kLs + (DKV ? kStages * 2 * kBN * 4 : 2 * kBM * 4);
     static constexpr int kMisc = kBars + (int)sizeof(Bars);
     static constexpr int kAlloc = kMisc + 64 + 1024;
     static_assert(kAlloc <= 232448, "shared memory budget");
@@ -82,8 +83,16 @@ struct Item {
     int first, kl;
     WinRow a, z;           // dQ: limits of the first and last row
     WinTiles wt;           // dQ: key tiles
-    int c0, per, steps;    // dK, dV: first query tile and tiles per query head; column tiles in all
+    int n;                 // dQ: their number, walked twice if a row sees few keys (below)
+    int c0, per, steps;    // dK, dV: first query tile and tiles per query head; steps in all
 };
+
+// D_i = dO_i . O_i carries the rounding of O to bf16, a share 2^-9 |O| |dO| that matters where a row
+// averages few values: at 4 visible keys it is as large as the rounding of dS, at 256 it is lost in
+// it.  A tile with such rows is walked twice: the first walk gives sum_j dS_ij = (exact D_i) - D_i in
+// fp32 (sum_j P_ij = 1), the second uses the corrected D_i, and so do dK and dV.  Those tiles are
+// short by nature.
+constexpr int kFewKeys = 256;
 
 template <bool DKV>
 __device__ __forceinline__ Item<DKV> item_of(const WinArgs &a, int it)
@@ -122,7 +131,10 @@ __device__ __forceinline__ Item<DKV> item_of(const WinArgs &a, int it)
         x.a = win_row(a, x.first + x.r0, x.kl);
         x.z = win_row(a, x.first + x.r0 + x.nrows - 1, x.kl);
         x.wt = win_tiles<kBN>(x.a, x.z);
-        x.steps = x.wt.count();
+        x.n = x.wt.count();
+        // the number of visible keys rises, stays and falls along the rows: least at an end
+        const int least = min(x.a.s + x.a.hi - x.a.lo, x.z.s + x.z.hi - x.z.lo);
+        x.steps = least < kFewKeys ? 2 * x.n : x.n;
     }
     return x;
 }
@@ -132,7 +144,7 @@ template <bool DKV>
 __device__ __forceinline__ int2 column_of(const WinArgs &a, const Item<DKV> &x, int t)
 {
     if (DKV) return make_int2(x.h * (a.H / a.Hkv) + t / x.per, (x.c0 + t % x.per) * kBN);
-    return make_int2(x.h / (a.H / a.Hkv), x.wt.at(t) * kBN);
+    return make_int2(x.h / (a.H / a.Hkv), x.wt.at(t < x.n ? t : t - x.n) * kBN);
 }
 
 // 32 values of this thread's row as bf16 pairs in 16 TMEM columns.
@@ -182,6 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&bars->land, 1);
         bar_init(&bars->out_full, 1);
         bar_init(&bars->out_free, 8);
+        bar_init(&bars->sums_full, 8);
+        bar_init(&bars->sums_free, 8);
         for (int s = 0; s < kMaxStages; ++s) {
             bar_init(&bars->c_full[s], 1);
             bar_init(&bars->c_empty[s], 1);
@@ -347,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int it = ring[slot];
                 bar_arrive(BAR(item_empty) + 8u * (slot));
                 if (it < 0) break;
-                const int steps = item_of<DKV>(a, it).steps;
+                const Item<DKV> x = item_of<DKV>(a, it);
+                const int steps = x.steps;
                 if (steps == 0) continue;
                 bool ok = true;
                 issued = true;
@@ -390,13 +405,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (T::kShared) mma_commit(BAR(s_free) + 8u * (w));
                         }
                         const uint64_t c1 = sw128_desc(cb, kBN * 128, 1024);
+                        const bool fresh = t == 0 || (!DKV && t == x.n);   // a walk's first step
                         ok = wait1(BAR(ds_full) + 8u * (w), use, W);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
                             mma_bf16_ts(out1, tmem + T::ds(g, kk), c1 + (uint64_t)(kk * 2048 >> 4), idesc_o,
-                                        (t > 0 || kk > 0) ? 1u : 0u);
+                                        (!fresh || kk > 0) ? 1u : 0u);
                         mma_commit(T::kShared ? BAR(d_free) + 8u * (w) : BAR(pd_free) + 8u * (w));
                         mma_commit(BAR(c_empty) + 8u * (s));
                         if (t == steps - 1) mma_commit(BAR(out_full));
@@ -420,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t items = 0;
         // the warpgroup's next step, with its buffers and their phases: S / dP buffer w, P / dS
         // buffer `odd`, column stage s
-        uint32_t mine = odd, w = odd, s = odd, use = 0, pd_use = 0, s_use = 0;
+        uint32_t mine = odd, w = odd, s = odd, use = 0, pd_use = 0, s_use = 0, sums_use = 0;
         for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
             const int it = next_item(item_k);
             if (it < 0) break;
@@ -442,16 +458,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ndelta = a.delta[ix];
                 }
             }
-            const unsigned long long c2 = f2pack(a.scale_log2, a.scale_log2), nlse2 = f2pack(nlse, nlse),
-                                     ndelta2 = f2pack(ndelta, ndelta);
-            bool ok = true;
+            const unsigned long long c2 = f2pack(a.scale_log2, a.scale_log2), nlse2 = f2pack(nlse, nlse);
+            unsigned long long ndelta2 = f2pack(ndelta, ndelta), sum2 = 0ull;
+            const bool twice = !DKV && x.steps > x.n;
+            bool ok = true, summing = twice;
+            // the end of a first walk: the rows' sums over both warpgroups' steps correct D
+            auto correct = [&]() {
+                float *sums = reinterpret_cast<float *>(sm + L::kSums);
+                const float2 part = f2unpack(sum2);
+                ok &= waitw(BAR(sums_free), (sums_use & 1) ^ 1, W);
+                sums[odd * kBM + row] = part.x + part.y;
+                __syncwarp();
+                warp_arrive(BAR(sums_full), lane);
+                ok &= waitw(BAR(sums_full), sums_use & 1, W);
+                ++sums_use;
+                ndelta -= sums[row] + sums[kBM + row];
+                __syncwarp();
+                warp_arrive(BAR(sums_free), lane);
+                ndelta2 = f2pack(ndelta, ndelta);
+                if (odd == 0 && valid) a.delta[win_row_index(a, x.b, x.h, x.r0 + row)] = ndelta;
+                summing = false;
+            };
             // this warpgroup's steps: mine, mine + 2, ... below g + steps.  The column tile follows
             // without a division: position `at` of the query tiles of a head (dK, dV)
             int at = (int)(mine - g);
             if constexpr (DKV)
                 while (at >= x.per && x.per > 0) at -= x.per;
             for (; ok && mine - g < (uint32_t)x.steps; mine += 2) {
-                const int j0 = (DKV ? (x.c0 + at) : x.wt.at((int)(mine - g))) * kBN;
+                if constexpr (!DKV) {
+                    at = (int)(mine - g);
+                    if (__builtin_expect(twice, 0) && at >= x.n) {
+                        if (summing) correct();
+                        at -= x.n;
+                    }
+                }
+                const int j0 = (DKV ? (x.c0 + at) : x.wt.at(at)) * kBN;
                 const uint32_t sb = tmem + lane_base + 128 * w;   // S; dP at + 64
                 const bool whole =
                     __all_sync(0xffffffffu, j0 + kBN <= lim.s || (lim.lo <= j0 && j0 + kBN <= lim.hi));
@@ -535,6 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < kBN; ++e) v[e] = (vis >> e) & 1ull ? v[e] : 0.f;
                 }
                 if constexpr (!DKV) {
+                    if (__builtin_expect(summing, 0)) {
+#pragma unroll
+                        for (int e = 0; e < kBN; e += 2) sum2 = f2add(sum2, f2pack(v[e], v[e + 1]));
+                    }
                     ok &= waitw(BAR(pd_free) + 8u * odd, pd_use ^ 1, W);
                     tc_fence_after();
                 }
@@ -566,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             g += x.steps;
+            if (summing && ok) correct();   // no step of the second walk was this warpgroup's
             if (!ok) break;
             // epilogue: dK by warpgroup 0 and dV by 1; of dQ, half the channels each
             if (x.steps > 0) {
