@@ -10,10 +10,11 @@
 //   warp 8           TMA of Q and K, and the item scheduler
 //   warp 9           TMA of V; zeroes the rows of edge tiles that no row of the item sees, so
 //                    that what lies there (0 x NaN) cannot reach the product
-//   warps 10 / 11    issue the products of Q tile 0 / 1 (one thread each)
+//   warps 10 / 11    issue S = Q K^T of Q tile 0 / 1, warps 12 / 13 P V (one thread each: after a
+//                    commit a thread's next wait takes some 400 cycles, in which the others'
+//                    products keep the tensor pipe fed)
 // TMEM: NSB buffers of S per Q tile (64 fp32 columns; P as bf16 pairs over the first 32 columns
-// of its own buffer) and two O tiles.  Per tile q the issuer runs S(0 .. NSB-1), then P V(t),
-// S(t + NSB): in the in-order tensor pipe S(t + NSB) cannot overwrite P(t) early.
+// of its own buffer) and two O tiles.  S(n + NSB) follows P V(n), which frees its buffer.
 // Only tiles that some row sees in part pay for the mask (one 64-bit word per row and tile).
 #include "window_tc.cuh"
 
@@ -23,12 +24,12 @@ namespace {
 
 constexpr int kBM = 128;           // queries per Q tile (TMEM lanes)
 constexpr int kBN = 64;            // keys per tile
-constexpr int kWarps = 12;
-constexpr int kThreads = kWarps * 32;
-constexpr int kLaunchRegs = 168;   // 65536 / 384, a multiple of 8; the split below sums to 384 x 168
-constexpr int kSoftmaxRegs = 216;  // 2 warpgroups x 128 threads
-constexpr int kOtherRegs = 72;     // 1 warpgroup
-static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "register split");
+constexpr int kThreads = 512;      // 16 warps, the last two idle (register splits are by warpgroup)
+constexpr int kItemWarps = 14;     // warps that read the items
+constexpr int kLaunchRegs = 128;   // 65536 / 512
+constexpr int kSoftmaxRegs = 192;  // 2 warpgroups x 128 threads
+constexpr int kOtherRegs = 64;     // 2 warpgroups
+static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * kLaunchRegs, "register split");
 constexpr int kMaxStages = 8, kMaxSB = 3, kRing = 4;
 constexpr uint32_t kTmemCols = 512;
 
@@ -42,7 +43,7 @@ struct __align__(8) Bars {
     uint64_t k_full[kMaxStages], k_empty[kMaxStages];
     uint64_t v_full[kMaxStages], v_empty[kMaxStages];
     uint64_t s_full[2][kMaxSB], p_full[2][kMaxSB], o_done[2][kMaxSB];
-    uint64_t o_free[2], drain[2];
+    uint64_t o_free[2], drain[4];
     uint64_t item_full[kRing], item_empty[kRing];
 };
 
@@ -152,11 +153,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bar_init(&bars->o_done[q][b], 1);
             }
             bar_init(&bars->o_free[q], 4);
-            bar_init(&bars->drain[q], 1);
         }
+        for (int k = 0; k < 4; ++k) bar_init(&bars->drain[k], 1);
         for (int k = 0; k < kRing; ++k) {
             bar_init(&bars->item_full[k], 1);
-            bar_init(&bars->item_empty[k], kWarps);
+            bar_init(&bars->item_empty[k], kItemWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -298,11 +299,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else {
             // -------------------------------------------------------------- product issuers
-            const int q = warp - 10;
+            const int q = warp & 1;
             bool issued = false;
-            if (lane == 0) {
+            if (lane == 0 && warp < 14) {
                 constexpr uint32_t idesc_qk = f16_idesc(kBM, kBN, false), idesc_pv = f16_idesc(kBM, D, true);
-                uint32_t k_it = 0, v_it = 0, q_it = 0, o_items = 0, p_par = 0;
+                uint32_t it_s = 0, items = 0;   // stages and items (with products) so far
+                uint32_t par = 0;               // bit b: parity of the next phase of buffer b that is waited for
                 const uint32_t s_base = tmem + q * NSB * kBN, o_tm = tmem + 2 * NSB * kBN + q * D;
                 const uint64_t qd = sw128_desc(sbase + L::kQ + q * L::kQTile, 16, 1024);
                 for (uint32_t item_k = 0; !*abort_flag; ++item_k) {
@@ -313,66 +315,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (it < 0) break;
                     const Item x = item_of(a, it, tiles);
                     if (x.t0 == x.t1) continue;
-                    if (!wait1(BAR(q_full), q_it & 1, W)) break;
-                    ++q_it;
-                    issued = true;
                     const WinTiles mine = pick(q == 1, x.q);
-                    int ns = 0, np = 0;   // S tiles and P V products issued for this Q tile
-                    auto qk_step = [&](int t) -> bool {
-                        const int ks = k_it % NS;
-                        if (!wait1(BAR(k_full) + 8u * (ks), (k_it / NS) & 1, W)) return false;
-                        if (sees(mine, x.all.at(t))) {
-                            tc_fence_after();
-                            const uint64_t kd = sw128_desc(sbase + L::kK + ks * L::kTile, 16, 1024);
-                            const int buf = ns % NSB;
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint64_t offa = (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
-                                const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
-                                mma_bf16(s_base + buf * kBN, qd + offa, kd + offb, idesc_qk, kk > 0);
-                            }
-                            mma_commit(BAR(s_full) + 8u * (kMaxSB * (q) + (buf)));
-                            ++ns;
-                        }
-                        mma_commit(BAR(k_empty) + 8u * (ks));
-                        if (t == x.t1 - 1) mma_commit(BAR(q_empty));
-                        ++k_it;
-                        return true;
-                    };
                     bool ok = true;
-                    for (int t = x.t0; t < min(x.t0 + NSB, x.t1) && ok; ++t) ok = qk_step(t);
-                    for (int t = x.t0; t < x.t1 && ok; ++t) {
-                        const int vs = v_it % NS;
-                        ok = wait1(BAR(v_full) + 8u * (vs), (v_it / NS) & 1, W);
-                        if (ok && sees(mine, x.all.at(t))) {
-                            const int buf = np % NSB;
-                            ok = wait1(BAR(p_full) + 8u * (kMaxSB * (q) + (buf)), (p_par >> buf) & 1u, W);
-                            if (ok && np == 0) {
-                                ok = wait1(BAR(o_free) + 8u * (q), (o_items & 1) ^ 1, W);
-                                ++o_items;
+                    int n = 0;   // this Q tile's products in the item
+                    issued = true;
+                    if (warp < 12) {
+                        // S(n) into buffer n % NSB, once P V has read what was there
+                        ok = wait1(BAR(q_full), items & 1, W);
+                        ++items;
+                        for (int t = x.t0; t < x.t1 && ok; ++t, ++it_s) {
+                            const int ks = it_s % NS;
+                            ok = wait1(BAR(k_full) + 8u * ks, (it_s / NS) & 1, W);
+                            if (ok && sees(mine, x.all.at(t))) {
+                                const int buf = n % NSB;
+                                ok = wait1(BAR(o_done) + 8u * (kMaxSB * q + buf), ((par >> buf) & 1u) ^ 1, W);
+                                if (!ok) break;
+                                par ^= 1u << buf;
+                                tc_fence_after();
+                                const uint64_t kd = sw128_desc(sbase + L::kK + ks * L::kTile, 16, 1024);
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk) {
+                                    const uint64_t offa = (uint64_t)(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) >> 4);
+                                    const uint64_t offb = (uint64_t)(((kk >> 2) * (kBN * 128) + (kk & 3) * 32) >> 4);
+                                    mma_bf16(s_base + buf * kBN, qd + offa, kd + offb, idesc_qk, kk > 0);
+                                }
+                                mma_commit(BAR(s_full) + 8u * (kMaxSB * q + buf));
+                                ++n;
                             }
-                            if (ok) {
-                                p_par ^= 1u << buf;
+                            if (!ok) break;
+                            mma_commit(BAR(k_empty) + 8u * ks);
+                            if (t == x.t1 - 1) mma_commit(BAR(q_empty));
+                        }
+                    } else {
+                        // O += P(n) V
+                        for (int t = x.t0; t < x.t1 && ok; ++t, ++it_s) {
+                            const int vs = it_s % NS;
+                            ok = wait1(BAR(v_full) + 8u * vs, (it_s / NS) & 1, W);
+                            if (ok && sees(mine, x.all.at(t))) {
+                                const int buf = n % NSB;
+                                ok = wait1(BAR(p_full) + 8u * (kMaxSB * q + buf), (par >> buf) & 1u, W);
+                                if (ok && n == 0) {
+                                    ok = wait1(BAR(o_free) + 8u * q, (items & 1) ^ 1, W);
+                                    ++items;
+                                }
+                                if (!ok) break;
+                                par ^= 1u << buf;
                                 tc_fence_after();
                                 const uint64_t vd = sw128_desc(sbase + L::kV + vs * L::kTile, kBN * 128, 1024);
 #pragma unroll
                                 for (int kk = 0; kk < kBN / 16; ++kk)
                                     mma_bf16_ts(o_tm, s_base + buf * kBN + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), idesc_pv,
-                                                (np > 0 || kk > 0) ? 1u : 0u);
-                                mma_commit(BAR(o_done) + 8u * (kMaxSB * (q) + (buf)));
-                                ++np;
+                                                (n > 0 || kk > 0) ? 1u : 0u);
+                                mma_commit(BAR(o_done) + 8u * (kMaxSB * q + buf));
+                                ++n;
                             }
+                            if (!ok) break;
+                            mma_commit(BAR(v_empty) + 8u * vs);
                         }
-                        if (!ok) break;
-                        mma_commit(BAR(v_empty) + 8u * (vs));
-                        ++v_it;
-                        if (t + NSB < x.t1) ok = qk_step(t + NSB);
                     }
                     if (!ok) break;
                 }
                 if (issued) {   // every product issued completes before TMEM is freed
-                    mma_commit(BAR(drain) + 8u * (q));
-                    drain_wait(BAR(drain) + 8u * (q), 0, W.limit_ns);
+                    mma_commit(BAR(drain) + 8u * (warp - 10));
+                    drain_wait(BAR(drain) + 8u * (warp - 10), 0, W.limit_ns);
                 }
             }
             __syncwarp();
