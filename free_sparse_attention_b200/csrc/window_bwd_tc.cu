@@ -21,6 +21,8 @@
 // P and dS are rounded to bf16 once, as operands; everything summed is fp32.
 #include "window_tc.cuh"
 
+#include <algorithm>
+
 namespace scope {
 
 namespace {
@@ -94,7 +96,7 @@ struct Item {
 // short by nature.
 constexpr int kFewKeys = 256;
 
-template <bool DKV>
+template <bool DKV, bool FEW>
 __device__ __forceinline__ Item<DKV> item_of(const WinArgs &a, int it)
 {
     Item<DKV> x;
@@ -134,7 +136,7 @@ __device__ __forceinline__ Item<DKV> item_of(const WinArgs &a, int it)
         x.n = x.wt.count();
         // the number of visible keys rises, stays and falls along the rows: least at an end
         const int least = min(x.a.s + x.a.hi - x.a.lo, x.z.s + x.z.hi - x.z.lo);
-        x.steps = least < kFewKeys ? 2 * x.n : x.n;
+        x.steps = FEW && least < kFewKeys ? 2 * x.n : x.n;
     }
     return x;
 }
@@ -164,7 +166,9 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const float *src, bool i
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
 
-template <bool DKV, int D>
+// FEW: some tile of the dQ pass may have rows that see few keys (the exact D costs every tile of
+// the pass 5 to 8 %, for the code it brings into the step loop, so it is left out where no row can).
+template <bool DKV, int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
     window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmR1, const __grid_constant__ CUtensorMap tmR2,
                          const __grid_constant__ CUtensorMap tmC1, const __grid_constant__ CUtensorMap tmC2,
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
                 const int it = next_item(item_k);
                 if (it < 0) break;
-                const Item<DKV> x = item_of<DKV>(a, it);
+                const Item<DKV> x = item_of<DKV, FEW>(a, it);
                 if (x.steps == 0) continue;
                 int ok = 1;
                 if (lane == 0) {
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int it = ring[slot];
                 bar_arrive(BAR(item_empty) + 8u * (slot));
                 if (it < 0) break;
-                const Item<DKV> x = item_of<DKV>(a, it);
+                const Item<DKV> x = item_of<DKV, FEW>(a, it);
                 const int steps = x.steps;
                 if (steps == 0) continue;
                 bool ok = true;
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (T::kShared) mma_commit(BAR(s_free) + 8u * (w));
                         }
                         const uint64_t c1 = sw128_desc(cb, kBN * 128, 1024);
-                        const bool fresh = t == 0 || (!DKV && t == x.n);   // a walk's first step
+                        const bool fresh = t == 0 || (FEW && t == x.n);   // a walk's first step
                         ok = wait1(BAR(ds_full) + 8u * (w), use, W);
                         if (!ok) break;
                         tc_fence_after();
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
             const int it = next_item(item_k);
             if (it < 0) break;
-            const Item<DKV> x = item_of<DKV>(a, it);
+            const Item<DKV> x = item_of<DKV, FEW>(a, it);
             const bool valid = row < x.nrows;
             auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
             // what the row sees: columns [0, s) and [lo, hi) (dQ) or [lo, hi) (dK, dV)
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const unsigned long long c2 = f2pack(a.scale_log2, a.scale_log2), nlse2 = f2pack(nlse, nlse);
             unsigned long long ndelta2 = f2pack(ndelta, ndelta), sum2 = 0ull;
-            const bool twice = !DKV && x.steps > x.n;
+            const bool twice = FEW && x.steps > x.n;
             bool ok = true, summing = twice;
             // the end of a first walk: the rows' sums over both warpgroups' steps correct D
             auto correct = [&]() {
@@ -484,15 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int at = (int)(mine - g);
             if constexpr (DKV)
                 while (at >= x.per && x.per > 0) at -= x.per;
-            for (; ok && mine - g < (uint32_t)x.steps; mine += 2) {
-                if constexpr (!DKV) {
-                    at = (int)(mine - g);
-                    if (__builtin_expect(twice, 0) && at >= x.n) {
-                        if (summing) correct();
-                        at -= x.n;
-                    }
-                }
-                const int j0 = (DKV ? (x.c0 + at) : x.wt.at(at)) * kBN;
+            for (uint32_t from = g, walks = FEW && x.steps > x.n ? 2 : 1; walks > 0 && ok; --walks) {
+            for (; ok && mine - from < (uint32_t)(DKV ? x.steps : x.n); mine += 2) {
+                const int j0 = (DKV ? (x.c0 + at) : x.wt.at((int)(mine - from))) * kBN;
                 const uint32_t sb = tmem + lane_base + 128 * w;   // S; dP at + 64
                 const bool whole =
                     __all_sync(0xffffffffu, j0 + kBN <= lim.s || (lim.lo <= j0 && j0 + kBN <= lim.hi));
@@ -576,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < kBN; ++e) v[e] = (vis >> e) & 1ull ? v[e] : 0.f;
                 }
                 if constexpr (!DKV) {
-                    if (__builtin_expect(summing, 0)) {
+                    if (FEW && __builtin_expect(summing, 0)) {
 #pragma unroll
                         for (int e = 0; e < kBN; e += 2) sum2 = f2add(sum2, f2pack(v[e], v[e + 1]));
                     }
@@ -610,8 +608,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     while (at >= x.per) at -= x.per;
                 }
             }
+            if constexpr (FEW) {
+                if (summing && ok) correct();
+                from += x.n;
+            }
+            }
             g += x.steps;
-            if (summing && ok) correct();   // no step of the second walk was this warpgroup's
             if (!ok) break;
             // epilogue: dK by warpgroup 0 and dV by 1; of dQ, half the channels each
             if (x.steps > 0) {
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WinArgs a)
     }
 }
 
-template <bool DKV, int D>
+template <bool DKV, int D, bool FEW>
 cudaError_t launch_pass(const WinArgs &a, cudaStream_t s)
 {
     CUtensorMap r1, r2, c1, c2;
@@ -706,14 +708,14 @@ cudaError_t launch_pass(const WinArgs &a, cudaStream_t s)
         !rows_map(&k, a.K, a.lk, a.B, a.Hkv, a.Nk, D, keys) || !rows_map(&v, a.V, a.lv, a.B, a.Hkv, a.Nk, D, keys))
         return cudaErrorInvalidValue;
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, window_bwd_tc_kernel<DKV, D>) != cudaSuccess || fa.numRegs != kLaunchRegs)
+    if (cudaFuncGetAttributes(&fa, window_bwd_tc_kernel<DKV, D, FEW>) != cudaSuccess || fa.numRegs != kLaunchRegs)
         return cudaErrorInvalidDeviceFunction;
     const long long items = DKV ? (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM) : (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM);
     if (items > 0x7ffffff0ll) return cudaErrorInvalidConfiguration;
     const int smem = Smem<DKV, D>::kAlloc;
-    cudaError_t e = cudaFuncSetAttribute(window_bwd_tc_kernel<DKV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(window_bwd_tc_kernel<DKV, D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    window_bwd_tc_kernel<DKV, D><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(r1, r2, c1, c2, a,
+    window_bwd_tc_kernel<DKV, D, FEW><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(r1, r2, c1, c2, a,
                                                                                                            (int)items);
     return cudaGetLastError();
 }
@@ -725,8 +727,15 @@ cudaError_t backward(const WinArgs &a, cudaStream_t s)
     const int per = 256 / (D / 8);
     window_delta_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_pass<false, D>(a, s);
-    if (e == cudaSuccess) e = launch_pass<true, D>(a, s);
+    // the first and the last query see the fewest keys
+    bool few = a.q_first || a.k_len;
+    for (const long long p : {(long long)a.first0, (long long)a.first0 + a.Nq - 1}) {
+        const long long f = p / a.frame, hi = std::min((long long)a.Nk, (f + a.right + 1) * a.frame),
+                        lo = std::min(hi, std::max(0ll, (f - a.left) * a.frame));
+        few = few || hi - lo + std::min(lo, (long long)a.sinks * a.frame) < kFewKeys;
+    }
+    if (e == cudaSuccess) e = few ? launch_pass<false, D, true>(a, s) : launch_pass<false, D, false>(a, s);
+    if (e == cudaSuccess) e = launch_pass<true, D, false>(a, s);
     return e;
 }
 
