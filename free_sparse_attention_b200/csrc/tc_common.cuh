@@ -264,6 +264,21 @@ __device__ __forceinline__ void tmem_wait_ld()
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// The same, and no use of v (the destination of the loads) moves ahead of the wait: the compiler
+// sees no dependence between the two otherwise.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[N])
+{
+    static_assert(N % 16 == 0, "in groups of 16");
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; i += 16)
+        asm volatile(""
+                     : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                       "+f"(v[i + 6]), "+f"(v[i + 7]), "+f"(v[i + 8]), "+f"(v[i + 9]), "+f"(v[i + 10]),
+                       "+f"(v[i + 11]), "+f"(v[i + 12]), "+f"(v[i + 13]), "+f"(v[i + 14]), "+f"(v[i + 15]));
+}
+
 __device__ __forceinline__ void tmem_wait_st()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");

@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float v[kBN];
                 tmem_ld32(sb, v);
                 tmem_ld32(sb + 32, v + 32);
-                tmem_wait_ld();
+                tmem_wait_ld(v);
                 if constexpr (!T::kShared) {
                     tc_fence_before();
                     __syncwarp();
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float dv[kBN];
                 tmem_ld32(sb + 64, dv);
                 tmem_ld32(sb + 96, dv + 32);
-                tmem_wait_ld();
+                tmem_wait_ld(dv);
                 if constexpr (!T::kShared) {
                     tc_fence_before();
                     __syncwarp();
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float o[16];
                 if (x.steps > 0) {
                     tmem_ld16(src + h * 16, o);
-                    tmem_wait_ld();
+                    tmem_wait_ld(o);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = 0.f;

@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s[kBN];
 #pragma unroll
                 for (int h = 0; h < kBN / 32; ++h) tmem_ld32(tmem + lane_base + sb_col + h * 32, s + h * 32);
-                tmem_wait_ld();
+                tmem_wait_ld(s);
                 if (__builtin_expect(!win_all(first_row, last_row, j0, j0 + kBN), 0)) {
                     // bit j: whether the row sees key j0 + j
                     auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int h = 0; h < D / 32; ++h) {
                         float o[32];
                         tmem_ld32(tmem + lane_base + o_col + h * 32, o);
-                        tmem_wait_ld();
+                        tmem_wait_ld(o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] *= alpha;
                         tmem_st32(tmem + lane_base + o_col + h * 32, o);
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float o[32];
                 if (n > 0) {
                     tmem_ld32(tmem + lane_base + o_col + h * 32, o);
-                    tmem_wait_ld();
+                    tmem_wait_ld(o);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0.f;
