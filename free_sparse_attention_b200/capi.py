@@ -411,15 +411,21 @@ def _current_stream(index):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
-def _tensors(fn, p, layouts, named):
+def _refuse(fn, name, t, shape, dt, where):
+    raise ValueError(f"{fn}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, wanted {shape} {dt} on {where}")
+
+
+def _tensors(fn, p, index, layouts, named):
     """The layouts argument of a strided call (None when every tensor is dense), after a check
-    of each (name, tensor, shape): device, type, shape and contiguous channels."""
+    of each (name, tensor, shape): device, type, shape and contiguous channels.  A tensor of None
+    is one that the call made itself: dense, with nothing to check."""
     dt = torch.bfloat16 if p.dtype == SCOPE_BF16 else torch.float32
-    index, lay = named[0][1].get_device(), None
+    lay = None
     for name, t, shape in named:
+        if t is None:
+            continue
         if t.shape != shape or t.dtype is not dt or t.get_device() != index or index < 0:
-            raise ValueError(f"{fn}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, wanted {shape} {dt} on "
-                             f"{named[0][1].device if index >= 0 else 'a GPU'}")
+            _refuse(fn, name, t, shape, dt, f"cuda:{index}" if index >= 0 else "a GPU")
         if not t.is_contiguous():
             st = t.stride()
             if st[3] != 1:
@@ -433,8 +439,7 @@ def _vector(fn, name, t, n, dtype, index):
     if t is None:
         return None
     if t.shape != (n,) or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, wanted ({n},) {dtype} on the "
-                         f"tensors' device {index}")
+        _refuse(fn, name, t, (n,), dtype, f"cuda:{index}")
     return t.data_ptr()
 
 
@@ -479,15 +484,15 @@ def qk_norm_rope3d(p, Q, K, w_q=None, w_k=None, first=None, out_q=None, out_k=No
         with torch.cuda.device(Q.device):
             return qk_norm_rope3d(p, Q, K, w_q, w_k, first, out_q, out_k, stream)
     fn, index, qs = "scope_qk_norm_rope3d", Q.get_device(), (p.B, p.H, p.N, p.d)
-    Yq = _new(Q, qs) if out_q is None else out_q
     if K is None:
         Yk = kp = yp = None
-        lay = _tensors(fn, p, QkNormLayouts, (("q", Q, qs), ("yq", Yq, qs)))
+        lay = _tensors(fn, p, index, QkNormLayouts, (("q", Q, qs), ("yq", out_q, qs)))
     else:
         ks = (p.B, p.Hkv, p.N, p.d)
+        lay = _tensors(fn, p, index, QkNormLayouts, (("q", Q, qs), ("yq", out_q, qs), ("k", K, ks), ("yk", out_k, ks)))
         Yk = _new(K, ks) if out_k is None else out_k
-        lay = _tensors(fn, p, QkNormLayouts, (("q", Q, qs), ("yq", Yq, qs), ("k", K, ks), ("yk", Yk, ks)))
         kp, yp = K.data_ptr(), Yk.data_ptr()
+    Yq = _new(Q, qs) if out_q is None else out_q
     _check(fn, lib().scope_qk_norm_rope3d(
         ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, index),
         _vector(fn, "w_k", w_k, p.d, torch.float32, index), _vector(fn, "first", first, p.B, torch.int32, index),
@@ -506,17 +511,16 @@ def qk_norm_rope3d_backward(p, Q, K, w_q, w_k, dYq, dYk, first=None, ws=None, ou
         raise ValueError(f"{fn}: K and dYk go together")
     ws = alloc_qk_norm_workspace(p, Q.device) if ws is None else ws
     _workspace(fn, ws, index)
+    ks = (p.B, p.Hkv, p.N, p.d)
+    lay = _tensors(fn, p, index, QkNormLayouts, (("q", Q, qs), ("yq", dYq, qs), ("dq", out_q, qs), ("k", K, ks),
+                                                 ("yk", dYk, ks), ("dk", out_k if K is not None else None, ks)))
     dQ = _new(Q, qs) if out_q is None else out_q
     dw = Q.new_empty((2, p.d), dtype=torch.float32)
     dwq = dw[0]
     if K is None:
         dK = dwk = kp = gp = dp = wp = None
-        lay = _tensors(fn, p, QkNormLayouts, (("q", Q, qs), ("yq", dYq, qs), ("dq", dQ, qs)))
     else:
-        ks = (p.B, p.Hkv, p.N, p.d)
         dK, dwk = _new(K, ks) if out_k is None else out_k, dw[1]
-        lay = _tensors(fn, p, QkNormLayouts, (("q", Q, qs), ("yq", dYq, qs), ("dq", dQ, qs), ("k", K, ks),
-                                              ("yk", dYk, ks), ("dk", dK, ks)))
         kp, gp, dp, wp = K.data_ptr(), dYk.data_ptr(), dK.data_ptr(), dwk.data_ptr()
     _check(fn, lib().scope_qk_norm_rope3d_backward(
         ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, index),
@@ -545,9 +549,9 @@ def window_attention(p, Q, K, V, q_first=None, k_len=None, ws=None, out=None, ls
     qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
     ws = alloc_window_workspace(p, Q.device) if ws is None else ws
     _workspace(fn, ws, index)
+    lay = _tensors(fn, p, index, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", out, qs)))
     O = _new(Q, qs) if out is None else out
     L = Q.new_empty(qs[:3], dtype=torch.float32) if lse else None
-    lay = _tensors(fn, p, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", O, qs)))
     _check(fn, lib().scope_window_attention(
         ctypes.byref(p), lay, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
         _vector(fn, "q_first", q_first, p.B, torch.int32, index), _vector(fn, "k_len", k_len, p.B, torch.int32, index),
@@ -566,11 +570,13 @@ def window_attention_backward(p, Q, K, V, O, dO, lse, q_first=None, k_len=None, 
     qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
     ws = alloc_window_workspace(p, Q.device) if ws is None else ws
     _workspace(fn, ws, index)
-    dQ, dK, dV = (_new(Q, qs), _new(K, ks), _new(V, ks)) if out is None else out
     if lse.shape != qs[:3] or lse.dtype is not torch.float32 or lse.get_device() != index or not lse.is_contiguous():
         raise ValueError(f"{fn}: lse is not a contiguous float32 tensor {qs[:3]} on the tensors' device {index}")
-    lay = _tensors(fn, p, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", O, qs), ("d_o", dO, qs),
-                                          ("dq", dQ, qs), ("dk", dK, ks), ("dv", dV, ks)))
+    dQ, dK, dV = (None, None, None) if out is None else out
+    lay = _tensors(fn, p, index, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", O, qs), ("d_o", dO, qs),
+                                                 ("dq", dQ, qs), ("dk", dK, ks), ("dv", dV, ks)))
+    if out is None:
+        dQ, dK, dV = _new(Q, qs), _new(K, ks), _new(V, ks)
     _check(fn, lib().scope_window_attention_backward(
         ctypes.byref(p), lay, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), lse.data_ptr(),
         _vector(fn, "q_first", q_first, p.B, torch.int32, index), _vector(fn, "k_len", k_len, p.B, torch.int32, index),

@@ -6,6 +6,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 using namespace scope;
@@ -44,12 +45,16 @@ scope_status cuda_status(cudaError_t e)
     return e == cudaSuccess ? SCOPE_OK : SCOPE_ERR_CUDA;
 }
 
+// SMs of the current device (a property that never changes: asked once per device).
 scope_status device_sms(int &sms)
 {
+    static std::atomic<int> known[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return SCOPE_ERR_CUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SCOPE_ERR_CUDA;
+    std::atomic<int> *slot = dev >= 0 && dev < 64 ? &known[dev] : nullptr;
+    if (slot && (sms = slot->load(std::memory_order_relaxed)) > 0) return SCOPE_OK;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SCOPE_ERR_CUDA;
+    if (slot) slot->store(sms, std::memory_order_relaxed);
     return SCOPE_OK;
 }
 
@@ -116,11 +121,16 @@ scope_status norm_args(const scope_qk_norm_params &p, const int32_t *first, Norm
     a.first = first;
     a.first0 = p.first;
     a.eps = (float)p.eps;
-    const int ranges[3] = {p.d_t, p.d_h, p.d_w};
-    const double lb = std::log2(p.base);
+    // turns per position of pair i of an axis: r^i / 2 pi, r = base^(-2 / width), by squares (a
+    // handful of roundings each)
     int k = 0;
-    for (int w : ranges)
-        for (int i = 0; i < w / 2; ++i) a.freq[k++] = std::exp2(-2.0 * i / w * lb) * 0.15915494309189535;   // / 2 pi
+    for (int w : {p.d_t, p.d_h, p.d_w}) {
+        double *f = a.freq + k;
+        const double r = w ? std::pow(p.base, -2.0 / w) : 1.0;
+        for (int i = 0; i < w / 2; ++i) f[i] = i == 0 ? 1.0 : (i & 1 ? f[i - 1] * r : f[i / 2] * f[i / 2]);
+        k += w / 2;
+    }
+    for (int i = 0; i < k; ++i) a.freq[i] *= 0.15915494309189535;
     return SCOPE_OK;
 }
 

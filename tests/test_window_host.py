@@ -131,7 +131,7 @@ def test_binding_refuses_tensors_that_do_not_fit():
     Q, K = torch.zeros((2, 4, 30, 64)), torch.zeros((2, 2, 40, 64))
     for args in ((Q, K, K), (Q.bfloat16(), K.bfloat16(), K.bfloat16())):      # float32; not on a GPU
         with pytest.raises(ValueError):
-            capi._tensors("f", p, capi.WindowLayouts, (("q", args[0], (2, 4, 30, 64)), ("k", args[1], (2, 2, 40, 64))))
+            capi._tensors("f", p, -1, capi.WindowLayouts, (("q", args[0], (2, 4, 30, 64)), ("k", args[1], (2, 2, 40, 64))))
     with pytest.raises(ValueError):
         capi._vector("f", "k_len", torch.zeros(3, dtype=torch.int32), 2, torch.int32, -1)
     with pytest.raises(ValueError):
