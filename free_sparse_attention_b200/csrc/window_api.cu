@@ -356,11 +356,10 @@ scope_status scope_window_attention(const scope_window_params *p, const scope_wi
     a.V = V;
     a.O = O;
     a.lse = lse;
+    if (a.is_bf16 && plan_of(*p).few) return cuda_status(window_few_forward(a, s));   // joins its shares itself
     cudaError_t e = cudaSuccess;
     if (!a.is_bf16) {
         e = window_simt_forward(a, s);
-    } else if (plan_of(*p).few) {
-        e = window_few_forward(a, s);
     } else {
         e = cudaMemsetAsync(ws, 0, kHeader, s);
         if (e == cudaSuccess) e = window_tc_forward(a, s);

@@ -7,11 +7,13 @@
 // 16 rows as M, a running maximum and sum per row in fp32, O += P V.  With 16 rows the legacy
 // matrix instructions take a fifth of the time the loads need; a tcgen05 tile would be 7/8 idle
 // rows and pay the TMEM round trip.  Two blocks share an SM: 3 tiles of 8 KB per warp keep
-// 128 KB of loads in flight there.  The warps join through shared memory, the shares in
-// window_join_kernel, in order.
+// 128 KB of loads in flight there.  The warps join through shared memory, and the shares of a unit,
+// up to 4, as one cluster through distributed shared memory, in order.
 // Rows of a 16-key tile lie at 2 d bytes, 16-byte chunk c of row r at c ^ (r mod 8): the 8 rows
 // of an ldmatrix meet different banks.
 #include "window.cuh"
+
+#include <cooperative_groups.h>
 
 namespace scope {
 
@@ -67,16 +69,18 @@ __device__ __forceinline__ float quad_sum(float v)
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-template <int D>
+// CLUSTER: the shares of a unit are one thread-block cluster and join through distributed shared
+// memory; otherwise window_join_kernel joins them.
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kFewWarps * 32, 2) window_few_kernel(WinArgs a)
 {
     constexpr int CH = D / 8;                       // 16-byte chunks of a row
     constexpr int kTileBytes = kTileKeys * D * 2;   // K or V
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float sm_m[kFewWarps][16], sm_l[kFewWarps][16];
+    __shared__ float sm_m[kFewWarps][16], sm_l[kFewWarps][16], sm_bm[16], sm_bl[16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tg = lane & 3, tr = lane >> 2;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;   // this path has no device conditions
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!CLUSTER) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
     const int groups = a.H / a.pack, b = unit / groups, h0 = (unit - b * groups) * a.pack, hk = h0 / (a.H / a.Hkv);
     const int rows = a.pack * a.Nq;
@@ -88,17 +92,25 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) window_few_kernel(WinArgs a
     const __nv_bfloat16 *kb = static_cast<const __nv_bfloat16 *>(a.K) + b * a.lk.b + hk * a.lk.h;
     const __nv_bfloat16 *vb = static_cast<const __nv_bfloat16 *>(a.V) + b * a.lv.b + hk * a.lv.h;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (kStages * 2 * kTileBytes);
+    // this lane's part of a tile: chunk `chunk` of rows lane_row, lane_row + step, ...
+    constexpr int STEP = 32 / CH > 0 ? 32 / CH : 1;
+    const int chunk = lane % CH, lane_row = lane / CH;
+    const __nv_bfloat16 *kl0 = kb + lane_row * a.lk.n + 8 * chunk, *vl0 = vb + lane_row * a.lv.n + 8 * chunk;
     auto issue = [&](int t, int s) {   // tile t (of this warp) into stage s; rows nobody sees become zeros
         if (t < t1) {
             const int j0 = wt.at(t) * kTileKeys;
             const uint32_t dst = ring + s * (2 * kTileBytes);
+            const __nv_bfloat16 *kp = kl0 + j0 * a.lk.n, *vp = vl0 + j0 * a.lv.n;
+            const bool whole = j0 + kTileKeys <= ra.s || (j0 >= ra.lo && j0 + kTileKeys <= rz.hi);
 #pragma unroll
-            for (int e = lane; e < kTileKeys * CH; e += 32) {
-                const int r = e / CH, c = e % CH, j = j0 + r;
-                const bool seen = j < ra.s || (j >= ra.lo && j < rz.hi);
-                const uint32_t off = r * (2 * D) + ((c ^ (r & 7)) << 4);
-                cp_async16(dst + off, seen ? kb + j * a.lk.n + 8 * c : kb, seen);
-                cp_async16(dst + kTileBytes + off, seen ? vb + j * a.lv.n + 8 * c : vb, seen);
+            for (int i = 0; i < kTileKeys / STEP; ++i) {
+                const int r = lane_row + i * STEP, j = j0 + r;
+                const bool seen = whole || j < ra.s || (j >= ra.lo && j < rz.hi);
+                const uint32_t off = r * (2 * D) + ((chunk ^ (r & 7)) << 4);
+                cp_async16(dst + off, seen ? kp : kb, seen);
+                cp_async16(dst + kTileBytes + off, seen ? vp : vb, seen);
+                kp += STEP * a.lk.n;
+                vp += STEP * a.lv.n;
             }
         }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
@@ -212,6 +224,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) window_few_kernel(WinArgs a
             *reinterpret_cast<float2 *>(so + (warp * 16 + tr + 8 * i) * D + c * 8 + 2 * tg) =
                 make_float2(o[c][2 * i], o[c][2 * i + 1]);
     __syncthreads();
+    // 4 channels of row r: out (already divided by the row sum), lse2 by the thread of channel 0
+    auto write = [&](int r, int c, const float (&x)[4], float lse2) {
+        const int h = h0 + r / a.Nq, q = r % a.Nq;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n + c;
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+        if (c == 0 && a.lse) a.lse[win_row_index(a, b, h, q)] = lse2 * 0.6931471805599453f;
+    };
     for (int e = threadIdx.x; e < rows * (D / 4); e += kFewWarps * 32) {
         const int r = e / (D / 4), c = (e % (D / 4)) * 4;
         float mm = -INFINITY;
@@ -229,40 +248,92 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) window_few_kernel(WinArgs a
             x[2] = fmaf(f, y.z, x[2]);
             x[3] = fmaf(f, y.w, x[3]);
         }
+        if (CLUSTER) {   // this share's row, for the cluster: the thread overwrites what it alone read
+            *reinterpret_cast<float4 *>(so + r * D + c) = make_float4(x[0], x[1], x[2], x[3]);
+            if (c == 0) {
+                sm_bm[r] = mm;
+                sm_bl[r] = sum;
+            }
+            continue;
+        }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const float lse2 = sum == 0.f ? -INFINITY : use + log2f(sum);
-        const int h = h0 + r / a.Nq, q = r % a.Nq;
-        const long long row = win_row_index(a, b, h, q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] *= inv;
         if (a.splits > 1) {
-            *reinterpret_cast<float4 *>(a.part_o + (row * a.splits + split) * D + c) =
-                make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+            const long long row = win_row_index(a, b, h0 + r / a.Nq, r % a.Nq);
+            *reinterpret_cast<float4 *>(a.part_o + (row * a.splits + split) * D + c) = make_float4(x[0], x[1], x[2], x[3]);
             if (c == 0) a.part_lse[row * a.splits + split] = lse2;
         } else {
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n + c;
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(x[0] * inv, x[1] * inv), pack2(x[2] * inv, x[3] * inv));
-            if (c == 0 && a.lse) a.lse[row] = lse2 * 0.6931471805599453f;
+            write(r, c, x, lse2);
         }
+    }
+    if constexpr (CLUSTER) {
+        // every block joins its part of the rows over all shares, in order
+        const auto cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        for (int e = split * (kFewWarps * 32) + threadIdx.x; e < rows * (D / 4); e += a.splits * (kFewWarps * 32)) {
+            const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+            float mm = -INFINITY;
+            for (int k = 0; k < a.splits; ++k) mm = fmaxf(mm, cluster.map_shared_rank(sm_bm, k)[r]);
+            const float use = mm == -INFINITY ? 0.f : mm;
+            float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < a.splits; ++k) {
+                const float f = exp2f(cluster.map_shared_rank(sm_bm, k)[r] - use);
+                const float4 y = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(so, k) + r * D + c);
+                sum = fmaf(f, cluster.map_shared_rank(sm_bl, k)[r], sum);
+                x[0] = fmaf(f, y.x, x[0]);
+                x[1] = fmaf(f, y.y, x[1]);
+                x[2] = fmaf(f, y.z, x[2]);
+                x[3] = fmaf(f, y.w, x[3]);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] *= inv;
+            write(r, c, x, sum == 0.f ? -INFINITY : use + log2f(sum));
+        }
+        cluster.sync();   // no block leaves while another reads its memory
     }
 }
 
-template <int D>
+template <int D, bool CLUSTER>
 cudaError_t launch(const WinArgs &a, cudaStream_t s)
 {
     const int smem = kFewWarps * kStages * 2 * kTileKeys * D * 2;
     static_assert(kFewWarps * 16 * D * 4 <= kFewWarps * kStages * 2 * kTileKeys * D * 2, "the join fits in the ring");
     const long long grid = (long long)a.B * (a.H / a.pack) * a.splits;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(window_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(window_few_kernel<D, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    window_few_kernel<D><<<(unsigned)grid, kFewWarps * 32, smem, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchAttribute shares{};
+    shares.id = cudaLaunchAttributeClusterDimension;
+    shares.val.clusterDim.x = (unsigned)a.splits;
+    shares.val.clusterDim.y = shares.val.clusterDim.z = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3(kFewWarps * 32);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &shares;
+    c.numAttrs = CLUSTER ? 1 : 0;
+    return cudaLaunchKernelEx(&c, window_few_kernel<D, CLUSTER>, a);
+}
+
+template <int D>
+cudaError_t forward(const WinArgs &a, cudaStream_t s)
+{
+    // Up to 4 shares as a cluster (16 x 8 units of 2: 50 us against 53 with a second kernel); larger
+    // clusters leave slots of a GPC empty (40 units of 7: 56 us against 39).
+    if (a.splits > 1 && a.splits <= 4) return launch<D, true>(a, s);
+    cudaError_t e = launch<D, false>(a, s);
+    return e == cudaSuccess && a.splits > 1 ? window_join(a, s) : e;
 }
 
 }  // namespace
 
 cudaError_t window_few_forward(const WinArgs &a, cudaStream_t s)
 {
-    return a.d == 64 ? launch<64>(a, s) : launch<128>(a, s);
+    return a.d == 64 ? forward<64>(a, s) : forward<128>(a, s);
 }
 
 }  // namespace scope
