@@ -96,29 +96,15 @@ struct Waiter {
     unsigned long long limit_ns;
 };
 
-// Test of an mbarrier phase that suspends the thread until the phase completes, for kTryNs at
-// most: a completed phase wakes it at once, and it takes no issue slots meanwhile.
-constexpr uint32_t kTryNs = 10000;
-__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(b)), "r"(parity), "r"(kTryNs)
-        : "memory");
-    return ok != 0;
-}
-
-// Bounded wait by one thread (as bar_wait, with the launch's limit).  The abort flag and the
-// timer, whose read takes hundreds of cycles, are looked at between suspended tests only.
+// Bounded wait by one thread (as bar_wait, with the launch's limit).
 __device__ __forceinline__ bool wait1(uint64_t *b, uint32_t parity, const Waiter &w)
 {
-    if (bar_try(b, parity)) return true;
+    if (bar_test(b, parity)) return true;
     const unsigned long long t0 = global_ns();
-    while (!bar_try(b, parity)) {
+    unsigned ns = 8;
+    while (!bar_test(b, parity)) {
+        __nanosleep(ns);
+        ns = ns < 64 ? ns * 2 : 64;
         if (*w.abort_flag) return false;
         if (global_ns() - t0 > w.limit_ns) {
             *w.abort_flag = 1;
@@ -129,16 +115,14 @@ __device__ __forceinline__ bool wait1(uint64_t *b, uint32_t parity, const Waiter
     return true;
 }
 
-// Warp-uniform wait: every lane tests (one instruction for the warp), and a vote makes the
-// answer the same for all; the waiting itself is lane 0's.
+// Warp-uniform wait: lane 0 polls, every lane gets the same answer.
 __device__ __forceinline__ bool waitw(uint64_t *b, uint32_t parity, const Waiter &w)
 {
-    if (__all_sync(0xffffffffu, bar_test(b, parity))) return true;
     int ok = 0;
     if ((threadIdx.x & 31) == 0) ok = wait1(b, parity, w) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
-    // the other lanes acquire the phase that lane 0 saw complete
-    return __all_sync(0xffffffffu, ok != 0 && bar_test(b, parity));
+    __syncwarp();
+    return ok != 0;
 }
 
 // A wait with no abort check, for draining work already issued (bounded all the same).
@@ -420,6 +404,9 @@ __device__ __forceinline__ bool bar_test(uint32_t b, uint32_t parity)
     return ok != 0;
 }
 
+// A test that suspends the thread until the phase completes, for kTryNs at most: a completed
+// phase wakes it at once, and it takes no issue slots meanwhile.
+constexpr uint32_t kTryNs = 10000;
 __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity)
 {
     uint32_t ok;
@@ -448,6 +435,8 @@ __device__ __forceinline__ void mma_commit(uint32_t b)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(b) : "memory");
 }
 
+// The abort flag and the timer, whose read takes hundreds of cycles, are looked at between
+// suspended tests only.
 __device__ __forceinline__ bool wait_long(uint32_t b, uint32_t parity, const Waiter &w)
 {
     if (bar_try(b, parity)) return true;
