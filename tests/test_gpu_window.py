@@ -261,12 +261,112 @@ def test_whole_layer_sampled_rows():
     frame against the binary64 form of those rows."""
     p = _params("bf16", H=6, Nq=17550, d=64, frame=1350, left=1, right=1, sinks=1)
     Q, K, V, _ = _inputs(p, "bf16", 29)
-    O = capi.window_attention(p, Q, K, V)
+    ws = capi.alloc_window_workspace(p)
+    O = capi.window_attention(p, Q, K, V, ws=ws)
+    assert capi.get_device_status(ws) == 0
     for r0 in (0, 1349, 8000, 17500):
         r1 = min(r0 + 50, 17550)
         pr = _params("bf16", H=6, Nq=r1 - r0, Nk=17550, d=64, frame=1350, left=1, right=1, sinks=1, q_first=r0)
         ref = attention(Q[:, :, r0:r1], K, V, visible(pr, [r0], [17550]))
         check("O", O[:, :, r0:r1], *ref["O"])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("left", [0, 1])
+def test_gaps_between_sinks_and_windows(left, d):
+    """Row tiles across frame ends: one half sees many key tiles in a row that the other does
+    not (more than the rings hold), behind the sinks and at the windows' ends."""
+    p = _params("bf16", H=2, Nq=5200, d=d, frame=1300, left=left, right=0, sinks=1)
+    Q, K, V, G = _inputs(p, "bf16", 41)
+    ws = capi.alloc_window_workspace(p)
+    O, lse = capi.window_attention(p, Q, K, V, ws=ws, lse=True)
+    assert capi.get_device_status(ws) == 0
+    grads = capi.window_attention_backward(p, Q, K, V, O, G, lse, ws=ws)
+    assert capi.get_device_status(ws) == 0
+    ref = attention(Q, K, V, visible(p, [0], [5200]), G)
+    check("O", O, *ref["O"])
+    for n, t in zip(("dQ", "dK", "dV"), grads):
+        check(n, t, *ref[n])
+
+
+def test_gradients_of_rows_that_see_few_keys():
+    """With 1 to 8 visible keys the rounding of O to bf16 would move D = dO . O as much as the
+    rounding of dS does: the bounds here count no error of D but binary32 sums'."""
+    p = _params("bf16", B=2, H=3, Nq=700, d=128, left=3, right=0, sinks=4)
+    Q, K, V, G = _inputs(p, "bf16", 43)
+    k_len = torch.tensor([700, 220], dtype=torch.int32, device="cuda")     # entry 1: most rows see sinks only
+    O, lse = capi.window_attention(p, Q, K, V, k_len=k_len, lse=True)
+    dQ, dK, dV = capi.window_attention_backward(p, Q, K, V, O, G, lse, k_len=k_len)
+    vis = visible(p, [0, 0], [700, 220]).cuda()[:, None]
+    q, k, v, g = (x.double() for x in (Q, K, V, G))
+    s = (q @ k.mT / math.sqrt(p.d)).masked_fill(~vis, -math.inf)
+    P = torch.nan_to_num(torch.softmax(s, -1))
+    dP = g @ v.mT
+    dS = P * (dP - (P * dP).sum(-1, keepdim=True))
+    # dS: one rounding to bf16; binary32 sums of 128 products in P (through the logits, at most
+    # 2 * 132 units of about 40 |.|) and in dP and D
+    bound = 2.0 ** -8 * dS.abs() + 2.0 ** -24 * P * (132 * (g.abs() @ v.abs().mT) * 2 + 600 * 8 * dP.abs().amax(-1, keepdim=True))
+    want = dS @ k / math.sqrt(p.d)
+    check("dQ", dQ, want, 2.0 ** -8 * want.abs() + 1.02 * (bound @ k.abs()) / math.sqrt(p.d))
+    want = dS.mT @ q / math.sqrt(p.d)
+    check("dK", dK, want, 2.0 ** -8 * want.abs() + 1.02 * (bound.mT @ q.abs()) / math.sqrt(p.d))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_beyond_32_bits(dtype):
+    """Batch entries 2^31 elements apart: every kernel's address arithmetic."""
+    dt, far = DT[dtype][0], 1 << 31
+    big = torch.empty(far + 4096 * 64, dtype=dt, device="cuda")
+
+    def place(x):
+        """x [2, h, n, 64] into slices of `big`, entry 1 at 2^31 elements, packed one after another."""
+        nonlocal used
+        h, n = x.shape[1], x.shape[2]
+        t = big.as_strided(x.shape, (far, n * 64, 64, 1), used)
+        t.copy_(x)
+        used += h * n * 64
+        return t
+
+    for Nq, Nk in ((150, 300), (1, 300)):
+        used = 0
+        p = _params(dtype, B=2, H=2, Nq=Nq, Nk=Nk, left=90, sinks=3, q_first=Nk - Nq)
+        Q, K, V, G = _inputs(p, dtype, 47)
+        dense, lse0 = capi.window_attention(p, Q, K, V, lse=True)
+        want = capi.window_attention_backward(p, Q, K, V, dense, G, lse0)
+        q, k, v, g = (place(x) for x in (Q, K, V, G))
+        o = place(torch.zeros_like(Q))
+        _, lse = capi.window_attention(p, q, k, v, out=o, lse=True)
+        assert torch.equal(o, dense) and torch.equal(lse, lse0)
+        outs = tuple(place(torch.zeros_like(x)) for x in (Q, K, V))
+        capi.window_attention_backward(p, q, k, v, o, g, lse, out=outs)
+        for x, y in zip(outs, want):
+            assert torch.equal(x, y)
+    used = 0
+    np_ = _norm_params(dtype, B=2, H=3, N=50)
+    X, G = _randn((2, 3, 50, 64), dt, 1), _randn((2, 3, 50, 64), dt, 2)
+    y0, _ = capi.qk_norm_rope3d(np_, X, None)
+    d0, _, w0, _ = capi.qk_norm_rope3d_backward(np_, X, None, None, None, G, None)
+    x, g, y, dx = place(X), place(G), place(torch.zeros_like(X)), place(torch.zeros_like(X))
+    capi.qk_norm_rope3d(np_, x, None, out_q=y)
+    _, _, w, _ = capi.qk_norm_rope3d_backward(np_, x, None, None, None, g, None, out_q=dx)
+    assert torch.equal(y, y0) and torch.equal(dx, d0) and torch.equal(w, w0)
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own, enqueued on two streams without waiting between."""
+    ps = [_params("bf16", H=4, Nq=900, d=128, left=300, sinks=4), _params("bf16", H=4, Nq=1, Nk=5000, d=128, left=-1, q_first=4999)]
+    ins = [_inputs(p, "bf16", 51 + i) for i, p in enumerate(ps)]
+    want = [capi.window_attention(p, *x[:3]) for p, x in zip(ps, ins)]
+    ws = [capi.alloc_window_workspace(p) for p in ps]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.empty_like(x[0]) for _ in range(20)] for x in ins]
+    torch.cuda.synchronize()
+    for r in range(20):
+        for p, x, w, s, o in zip(ps, ins, ws, streams, outs):
+            capi.window_attention(p, *x[:3], ws=w, out=o[r], stream=s)
+    torch.cuda.synchronize()
+    for o, y in zip(outs, want):
+        assert all(torch.equal(t, y) for t in o)
 
 
 # ------------------------------------------------------------------------------ norm + RoPE
