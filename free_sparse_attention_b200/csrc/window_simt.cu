@@ -8,10 +8,10 @@
 // shared memory with rows padded by 4 floats, so that the 16-byte reads of 16 neighbouring
 // rows meet different banks.  A thread owns rows ty + 8 i and columns tx + 16 j of a score tile
 // (4 x 4 scores from 8 16-byte reads per 4 channels, 64 FMAs in 32 packed instructions), and rows ty + 8 i and channels
-// 4 tx + 64 j .. + 3 of an output.  Tiles arrive by cp.async as soon as their place is free, and
-// two blocks (four at d = 64) share an SM, so that one computes while the other waits.  Scores,
-// softmax statistics and all sums are fp32.  Bound by the FMA pipe (74 TFLOP/s) and, next to it,
-// by the shared-memory reads that feed it.
+// 4 tx + 64 j .. + 3 of an output.  Tiles arrive by cp.async as soon as their place is free (K and V
+// of a tile in turn in one place), and two to four blocks share an SM, so that one computes while
+// another waits.  Scores, softmax statistics and all sums are fp32.  Bound by the FMA pipe (61 % busy
+// in the forward of 2 x 6 heads x 1777 rows, d 64, window 300: 87 us) and the tiles' masked parts.
 #include "window.cuh"
 
 namespace scope {
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kTh) window_fwd_kernel(WinArgs a)
     extern __shared__ __align__(16) float sm[];
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;   // this path has no device conditions
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    float *sq = sm, *sk = sq + BM * (D + 4), *sv = sk + kBN * (D + 4), *sp = sv + kBN * (D + 4);
+    float *sq = sm, *sc = sq + BM * (D + 4), *sp = sc + kBN * (D + 4);   // sc: K, then V of a tile
     const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
     const int rows = a.pack * a.Nq, tiles = (rows + BM - 1) / BM;
     // item = ((unit * tiles) + tile) * splits + split
@@ -212,8 +212,7 @@ __global__ void __launch_bounds__(kTh) window_fwd_kernel(WinArgs a)
         const int rr = r0 + r;
         return rr < r1 ? qb + (h0 + rr / a.Nq) * a.lq.h + (rr % a.Nq) * a.lq.n : nullptr;
     });
-    keys(sk, kb, a.lk.n, t0);
-    keys(sv, vb, a.lv.n, t0);
+    keys(sc, kb, a.lk.n, t0);
     WinRow lim[MI];
     float m[MI], l[MI];
     uint64_t o[MI][D / 32];
@@ -228,11 +227,11 @@ __global__ void __launch_bounds__(kTh) window_fwd_kernel(WinArgs a)
     }
     for (int t = t0; t < t1; ++t) {
         const int j0 = wt.at(t) * kBN;
-        arrived<1>();
+        arrived<0>();
         float s[MI][4];
-        scores<D, MI>(s, sq, sk, ty, tx);
+        scores<D, MI>(s, sq, sc, ty, tx);
         __syncthreads();
-        keys(sk, kb, a.lk.n, t + 1);
+        keys(sc, vb, a.lv.n, t);
         const bool all = win_all(ra, rz, j0, j0 + kBN);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
@@ -261,10 +260,10 @@ __global__ void __launch_bounds__(kTh) window_fwd_kernel(WinArgs a)
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) o[i][e] = fma2(o[i][e], c2, 0ull);
         }
-        arrived<1>();
-        accumulate<D, MI>(o, sp, sv, ty, tx);
+        arrived<0>();
+        accumulate<D, MI>(o, sp, sc, ty, tx);
         __syncthreads();
-        keys(sv, vb, a.lv.n, t + 1);
+        keys(sc, kb, a.lk.n, t + 1);
     }
     arrived<0>();
 #pragma unroll
@@ -334,7 +333,7 @@ __global__ void __launch_bounds__(kTh) window_dq_kernel(WinArgs a)
     constexpr int MI = kBM / 8;
     extern __shared__ __align__(16) float sm[];
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
-    float *sq = sm, *sg = sq + kBM * (D + 4), *sk = sg + kBM * (D + 4), *sv = sk + kBN * (D + 4), *sp = sv + kBN * (D + 4);
+    float *sq = sm, *sg = sq + kBM * (D + 4), *sc = sg + kBM * (D + 4), *sp = sc + kBN * (D + 4);   // sc: V, then K of a tile
     const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
     const int tiles = (a.Nq + kBM - 1) / kBM;
     const int tile = (int)(blockIdx.x % tiles), bh = (int)(blockIdx.x / tiles);
@@ -358,9 +357,8 @@ __global__ void __launch_bounds__(kTh) window_dq_kernel(WinArgs a)
     };
     load_tile<D, kBM>(sq, qb, [&](int r) -> const float * { return r0 + r < r1 ? qb + (r0 + r) * a.lq.n : nullptr; });
     load_tile<D, kBM>(sg, gb, [&](int r) -> const float * { return r0 + r < r1 ? gb + (r0 + r) * a.lg.n : nullptr; });
-    keys(sv, vb, a.lv.n, 0);
-    keys(sk, kb, a.lk.n, 0);
-    arrived<2>();
+    keys(sc, vb, a.lv.n, 0);
+    arrived<1>();
     WinRow lim[MI];
     float lse[MI], dl[MI];
     uint64_t dq[MI][D / 32];
@@ -389,12 +387,13 @@ __global__ void __launch_bounds__(kTh) window_dq_kernel(WinArgs a)
     }
     for (int t = 0; t < nt; ++t) {
         const int j0 = wt.at(t) * kBN;
-        arrived<1>();
-        float s[MI][4], dp[MI][4];
-        scores<D, MI>(dp, sg, sv, ty, tx);
         arrived<0>();
-        keys(sv, vb, a.lv.n, t + 1);
-        scores<D, MI>(s, sq, sk, ty, tx);
+        float s[MI][4], dp[MI][4];
+        scores<D, MI>(dp, sg, sc, ty, tx);
+        __syncthreads();
+        keys(sc, kb, a.lk.n, t);
+        arrived<0>();
+        scores<D, MI>(s, sq, sc, ty, tx);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -405,9 +404,9 @@ __global__ void __launch_bounds__(kTh) window_dq_kernel(WinArgs a)
                     vis ? exp2f(fmaf(s[i][j], a.scale_log2, -lse[i])) * (dp[i][j] - dl[i]) : 0.f;
             }
         __syncwarp();   // a row of sp is written and read by one warp
-        accumulate<D, MI>(dq, sp, sk, ty, tx);
+        accumulate<D, MI>(dq, sp, sc, ty, tx);
         __syncthreads();
-        keys(sk, kb, a.lk.n, t + 1);
+        keys(sc, vb, a.lv.n, t + 1);
     }
     arrived<0>();
     float *dst = static_cast<float *>(a.dQ) + b * a.ldq.b + h * a.ldq.h;
@@ -521,16 +520,17 @@ cudaError_t forward(const WinArgs &a, cudaStream_t s)
     // 16-row tiles when a unit's rows fill no more than one
     const long long rows = (long long)a.pack * a.Nq, units = (long long)a.B * (a.H / a.pack);
     if (rows <= 16)
-        return launch(window_fwd_kernel<D, 16>, units * a.splits, (16 + 2 * kBN) * (D + 4) * 4 + 16 * kLdP * 4, a, s);
+        return launch(window_fwd_kernel<D, 16>, units * a.splits, (16 + kBN) * (D + 4) * 4 + 16 * kLdP * 4, a, s);
     return launch(window_fwd_kernel<D, kBM>, units * ((rows + kBM - 1) / kBM) * a.splits,
-                  (kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s);
+                  (kBM + kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s);
 }
 
 template <int D>
 cudaError_t backward(const WinArgs &a, cudaStream_t s)
 {
     const int smem = (2 * kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4;
-    cudaError_t e = launch(window_dq_kernel<D>, (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM), smem, a, s);
+    cudaError_t e = launch(window_dq_kernel<D>, (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM),
+                           (2 * kBM + kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s);
     if (e != cudaSuccess) return e;
     return launch(window_dkv_kernel<D>, (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM), smem, a, s);
 }
