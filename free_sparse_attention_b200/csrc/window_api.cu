@@ -168,9 +168,12 @@ Plan plan_of(const scope_window_params &p)
 {
     Plan r;
     const int G = p.H / p.Hkv;
-    // few rows: the query heads of one key head share a tile, so that its keys are read once
-    r.few = (long long)G * p.Nq <= 16;
-    r.pack = r.few ? G : 1;
+    // few rows: as many query heads of one key head as fill 16 rows share a tile, so that the keys
+    // are read once for all of them (in equal packs)
+    r.few = p.Nq <= 16;
+    r.pack = 1;
+    for (int n = 2; r.few && n <= G && n * p.Nq <= 16; ++n)
+        if (G % n == 0) r.pack = n;
     // rows of one item and keys of one of its tiles: few rows, tensor cores, or fp32; items
     // that the device holds at a time
     const bool bf16 = p.dtype == SCOPE_BF16;

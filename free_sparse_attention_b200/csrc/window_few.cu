@@ -1,5 +1,5 @@
-// Window attention for few query rows over a long cache (bf16): up to 16 rows, the query heads of
-// one key head together, so that every key and value is read once.
+// Window attention for few query rows over a long cache (bf16): tiles of up to 16 rows, query heads
+// of one key head together, so that a key and its value are read once for all of them.
 //
 // Bound by HBM: 4 d bytes per key and key head against 4 d flops per row.  A block of 4 warps
 // owns one share of the unit's keys; each warp walks its own 16-key tiles through its own ring

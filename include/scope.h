@@ -415,6 +415,8 @@ scope_status scope_tc_accumulation_probe(const void *A, const void *B, int K, in
  *    positions of first tokens <= 2^30 (else SCOPE_ERR_UNSUPPORTED).
  *  - Outputs must not overlap inputs, except where stated.  Sums are taken in a fixed order:
  *    the same call gives the same bits.
+ *  - The first call on a device loads the library's device code there: make it before any stream
+ *    capture.
  */
 typedef struct {
     int64_t batch, head, token;
@@ -499,9 +501,10 @@ size_t scope_window_workspace_bytes(const scope_window_params *p);
  *            p->q_first (values outside [0, 2^30] are clamped)
  *   k_len    [B] int32 (device) keys of each entry, or NULL for Nk (clamped to [0, Nk])
  *   lse      out [B,H,Nq] float log sum exp of each row's scaled logits (-inf: no key), or NULL
- * Keys and values at or beyond k_len may hold anything.  Keys that a query does not see do not
- * touch its output; a value row that is not finite can reach the outputs of other queries
- * of the same 256 that do see a neighbouring key.
+ * Keys and values at or beyond k_len, and all others that no query sees, may hold anything.  A key
+ * that a query does not see never touches its output; a value that is not finite makes the
+ * outputs not finite of the queries that see it, and can make those of other queries of the same
+ * run of 256 so.  bf16 rounds P to bf16 for P V; sums and statistics are fp32.
  */
 scope_status scope_window_attention(const scope_window_params *p, const scope_window_layouts *lay, const void *Q,
                                     const void *K, const void *V, const int32_t *q_first, const int32_t *k_len, void *O,
@@ -511,8 +514,11 @@ scope_status scope_window_attention(const scope_window_params *p, const scope_wi
  * Gradients from dO and the forward's inputs, O and lse:  with P = exp(s - lse) and
  * D_i = dO_i . O_i,  dV = P^T dO,  dS = P o (dO V^T - D),  dQ = dS K / sqrt d,
  * dK = dS^T Q / sqrt d; dK and dV summed over the query heads of their group.  Every row is
- * written: zeros for queries that see no key and keys that no query sees.
+ * written: zeros for queries that see no key and keys that no query sees.  Q, O and dO must be
+ * finite (a padded batch's spare rows too: zeros in dO leave them without effect).
  *   dO [B,H,Nq,d] dtype; dQ like Q, dK, dV like K, V (dtype)
+ * bf16 rounds P and dS to bf16, once each, for the products; D is exact to fp32 where a query sees
+ * fewer than 256 keys, and that of the rounded O elsewhere.
  */
 scope_status scope_window_attention_backward(const scope_window_params *p, const scope_window_layouts *lay,
                                              const void *Q, const void *K, const void *V, const void *O, const void *dO,
