@@ -10,8 +10,10 @@
 // (4 x 4 scores from 8 16-byte reads per 4 channels, 64 FMAs in 32 packed instructions), and rows ty + 8 i and channels
 // 4 tx + 64 j .. + 3 of an output.  Tiles arrive by cp.async as soon as their place is free (K and V
 // of a tile in turn in one place), and two to four blocks share an SM, so that one computes while
-// another waits.  Scores, softmax statistics and all sums are fp32.  Bound by the FMA pipe (61 % busy
-// in the forward of 2 x 6 heads x 1777 rows, d 64, window 300: 87 us) and the tiles' masked parts.
+// another waits.  Scores, softmax statistics and all sums are fp32.  Bound by the FMA pipe (82 % busy
+// on an SM with three blocks), the tiles' masked parts and the last blocks' end: the forward of 2 x 6
+// heads x 1777 rows, d 64, window 300, takes 81 us; 8 heads x 1430 rows, d 128, frames of 143, two before
+// and one after: forward 164 us and 9 to join, gradients 454 us and 4 for D.
 #include "window.cuh"
 
 namespace scope {
@@ -102,42 +104,77 @@ __device__ __forceinline__ ulonglong2 load22(const float *p)
     return *reinterpret_cast<const ulonglong2 *>(p);
 }
 
-// acc[i][j] = rows[ty + 8 i] . cols[tx + 16 j]: even and odd channels summed apart.
-template <int D, int MI>
-__device__ __forceinline__ void scores(float (&acc)[MI][4], const float *rows, const float *cols, int ty, int tx)
+// acc[i][j] = rows[ty + 8 i] . cols[tx + 16 j], j < NJ: even and odd channels summed apart.
+template <int D, int MI, int NJ>
+__device__ __forceinline__ void scores_of(float (&acc)[MI][4], const float *rows, const float *cols, int ty, int tx)
 {
-    uint64_t s[MI][4];
+    uint64_t s[MI][NJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0ull;
+        for (int j = 0; j < NJ; ++j) s[i][j] = 0ull;
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-        ulonglong2 x[MI], y[4];
+        ulonglong2 x[MI], y[NJ];
 #pragma unroll
         for (int i = 0; i < MI; ++i) x[i] = load22(rows + (ty + 8 * i) * (D + 4) + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = load22(cols + (tx + 16 * j) * (D + 4) + c);
+        for (int j = 0; j < NJ; ++j) y[j] = load22(cols + (tx + 16 * j) * (D + 4) + c);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, s[i][j]));
+            for (int j = 0; j < NJ; ++j) s[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, s[i][j]));
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 f = unpair(s[i][j]);
+            const float2 f = j < NJ ? unpair(s[i][j < NJ ? j : 0]) : make_float2(0.f, 0.f);
             acc[i][j] = f.x + f.y;
         }
 }
 
-// out[i][2 jj], [2 jj + 1] (channels 4 tx + 64 jj .. + 3 in pairs) += sum_k w[ty + 8 i][k] cols[k][...]
-template <int D, int MI>
-__device__ __forceinline__ void accumulate(uint64_t (&out)[MI][D / 32], const float *w, const float *cols, int ty, int tx)
+// Groups of 16 columns of a tile that some row of the block meets: tiles at a window's edges and the
+// last of the sinks are often partly empty, and half a tile or more that nobody sees is left out.
+struct Groups {
+    int lo, n;   // groups lo .. lo + n - 1: one, two or all four
+};
+
+__device__ __forceinline__ Groups groups(int lo, int end)
 {
+    return end - lo > 2 ? Groups{0, 4} : Groups{lo, end - lo};
+}
+
+// The groups of key tile j0 between rows ra (first) and rz (last).
+__device__ __forceinline__ Groups key_groups(const WinRow &ra, const WinRow &rz, int j0)
+{
+    const int lo = j0 < ra.s ? 0 : max(0, ra.lo - j0) >> 4;
+    const int end = max(min(ra.s - j0, kBN), ra.lo < j0 + kBN ? min(rz.hi - j0, kBN) : 0);
+    return groups(min(lo, 3), max(min(lo, 3) + 1, (end + 15) >> 4));
+}
+
+// acc[i][j] = rows[ty + 8 i] . cols[16 (g.lo + j) + tx], j < g.n; zeros for the others.
+template <int D, int MI>
+__device__ __forceinline__ void scores(float (&acc)[MI][4], const float *rows, const float *cols, int ty, int tx, Groups g)
+{
+    cols += 16 * g.lo * (D + 4);
+    if (g.n == 4)
+        scores_of<D, MI, 4>(acc, rows, cols, ty, tx);
+    else if (g.n == 2)
+        scores_of<D, MI, 2>(acc, rows, cols, ty, tx);
+    else
+        scores_of<D, MI, 1>(acc, rows, cols, ty, tx);
+}
+
+// out[i][2 jj], [2 jj + 1] (channels 4 tx + 64 jj .. + 3 in pairs) += sum_k w[ty + 8 i][k] cols[k][...],
+// k over the columns of the groups; w[.][k] starts at the first of them.
+template <int D, int MI>
+__device__ __forceinline__ void accumulate(uint64_t (&out)[MI][D / 32], const float *w, const float *cols, int ty, int tx, Groups g)
+{
+    cols += 16 * g.lo * (D + 4);
+    const int n = 16 * g.n;
 #pragma unroll 2
-    for (int k = 0; k < kBN; k += 4) {
+    for (int k = 0; k < n; k += 4) {
         float4 p[MI];
 #pragma unroll
         for (int i = 0; i < MI; ++i) p[i] = load4(w + (ty + 8 * i) * kLdP + k);
@@ -172,7 +209,7 @@ __device__ __forceinline__ void store_scaled(float *p, const uint64_t *v, float 
 // Forward: BM rows of one unit (b, group of a.pack query heads) against one share of the key
 // tiles they see.  BM = 32, or 16 (two rows per thread) where a unit's rows fill no more.
 template <int D, int BM>
-__global__ void __launch_bounds__(kTh) window_fwd_kernel(WinArgs a)
+__global__ void __launch_bounds__(kTh, D == 64 ? 4 : 3) window_fwd_kernel(WinArgs a)
 {
     constexpr int MI = BM / 8;
     extern __shared__ __align__(16) float sm[];
@@ -228,8 +265,9 @@ __global__ void __launch_bounds__(kTh) window_fwd_kernel(WinArgs a)
     for (int t = t0; t < t1; ++t) {
         const int j0 = wt.at(t) * kBN;
         arrived<0>();
+        const Groups g = key_groups(ra, rz, j0);
         float s[MI][4];
-        scores<D, MI>(s, sq, sc, ty, tx);
+        scores<D, MI>(s, sq, sc, ty, tx, g);
         __syncthreads();
         keys(sc, vb, a.lv.n, t);
         const bool all = win_all(ra, rz, j0, j0 + kBN);
@@ -238,8 +276,8 @@ __global__ void __launch_bounds__(kTh) window_fwd_kernel(WinArgs a)
             float mt = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int key = j0 + tx + 16 * j;
-                const bool vis = all || key < lim[i].s || (key >= lim[i].lo && key < lim[i].hi);
+                const int key = j0 + 16 * (g.lo + j) + tx;
+                const bool vis = all || (j < g.n && (key < lim[i].s || (key >= lim[i].lo && key < lim[i].hi)));
                 s[i][j] = vis ? s[i][j] * a.scale_log2 : -INFINITY;
                 mt = fmaxf(mt, s[i][j]);
             }
@@ -261,7 +299,7 @@ __global__ void __launch_bounds__(kTh) window_fwd_kernel(WinArgs a)
             for (int e = 0; e < D / 32; ++e) o[i][e] = fma2(o[i][e], c2, 0ull);
         }
         arrived<0>();
-        accumulate<D, MI>(o, sp, sc, ty, tx);
+        accumulate<D, MI>(o, sp, sc, ty, tx, g);
         __syncthreads();
         keys(sc, kb, a.lk.n, t + 1);
     }
@@ -326,17 +364,33 @@ __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a)
     if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
-// dQ: 32 query rows of one head against the key tiles they see; also writes D_i.
+// D_i = dO_i . O_i, one warp per row.
 template <int D>
-__global__ void __launch_bounds__(kTh) window_dq_kernel(WinArgs a)
+__global__ void __launch_bounds__(kTh) window_delta_kernel(WinArgs a)
+{
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long row = (long long)blockIdx.x * (kTh / 32) + (threadIdx.x >> 5);
+    if (row >= (long long)a.B * a.H * a.Nq) return;
+    const int i = (int)(row % a.Nq), h = (int)(row / a.Nq % a.H), b = (int)(row / a.Nq / a.H), c = 4 * (threadIdx.x & 31);
+    float s = 0.f;
+    if (c < D)
+        dot4(s, load4(static_cast<const float *>(a.O) + b * a.lo.b + h * a.lo.h + i * a.lo.n + c),
+             load4(static_cast<const float *>(a.G) + b * a.lg.b + h * a.lg.h + i * a.lg.n + c));
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    if (c == 0) a.delta[row] = s;
+}
+
+// dQ: 32 query rows of one head against the key tiles they see.
+template <int D>
+__device__ __forceinline__ void dq_block(const WinArgs &a, float *sm, long long block)
 {
     constexpr int MI = kBM / 8;
-    extern __shared__ __align__(16) float sm[];
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     float *sq = sm, *sg = sq + kBM * (D + 4), *sc = sg + kBM * (D + 4), *sp = sc + kBN * (D + 4);   // sc: V, then K of a tile
     const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
     const int tiles = (a.Nq + kBM - 1) / kBM;
-    const int tile = (int)(blockIdx.x % tiles), bh = (int)(blockIdx.x / tiles);
+    const int tile = (int)(block % tiles), bh = (int)(block / tiles);
     const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hkv);
     const int r0 = tile * kBM, r1 = min(a.Nq, r0 + kBM);
     const int first = win_first(a, b), kl = win_klen(a, b);
@@ -369,42 +423,31 @@ __global__ void __launch_bounds__(kTh) window_dq_kernel(WinArgs a)
         lim[i] = in ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
         const long long row = win_row_index(a, b, h, in ? q : r0);
         lse[i] = in ? a.lse[row] * 1.4426950408889634f : -INFINITY;
-        float s = 0.f;
-        if (in) {
-            const float *ob = static_cast<const float *>(a.O) + b * a.lo.b + h * a.lo.h + q * a.lo.n;
-#pragma unroll
-            for (int jj = 0; jj < D / 64; ++jj) {
-                const int c = 4 * tx + 64 * jj;
-                dot4(s, load4(ob + c), load4(sg + (ty + 8 * i) * (D + 4) + c));
-            }
-        }
-#pragma unroll
-        for (int x = 16; x > 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        dl[i] = s;
-        if (in && tx == 0) a.delta[row] = s;
+        dl[i] = in ? a.delta[row] : 0.f;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) dq[i][e] = 0ull;
     }
     for (int t = 0; t < nt; ++t) {
         const int j0 = wt.at(t) * kBN;
         arrived<0>();
+        const Groups g = key_groups(ra, rz, j0);
         float s[MI][4], dp[MI][4];
-        scores<D, MI>(dp, sg, sc, ty, tx);
+        scores<D, MI>(dp, sg, sc, ty, tx, g);
         __syncthreads();
         keys(sc, kb, a.lk.n, t);
         arrived<0>();
-        scores<D, MI>(s, sq, sc, ty, tx);
+        scores<D, MI>(s, sq, sc, ty, tx, g);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int key = j0 + tx + 16 * j;
-                const bool vis = key < lim[i].s || (key >= lim[i].lo && key < lim[i].hi);
+                const int key = j0 + 16 * (g.lo + j) + tx;
+                const bool vis = j < g.n && (key < lim[i].s || (key >= lim[i].lo && key < lim[i].hi));
                 sp[(ty + 8 * i) * kLdP + tx + 16 * j] =
                     vis ? exp2f(fmaf(s[i][j], a.scale_log2, -lse[i])) * (dp[i][j] - dl[i]) : 0.f;
             }
         __syncwarp();   // a row of sp is written and read by one warp
-        accumulate<D, MI>(dq, sp, sc, ty, tx);
+        accumulate<D, MI>(dq, sp, sc, ty, tx, g);
         __syncthreads();
         keys(sc, vb, a.lv.n, t + 1);
     }
@@ -423,15 +466,14 @@ __global__ void __launch_bounds__(kTh) window_dq_kernel(WinArgs a)
 // dK, dV: 32 keys of one key head against every query (of all its query heads, in order) that
 // may see one of them.  Scores are taken transposed: rows are keys, columns are queries.
 template <int D>
-__global__ void __launch_bounds__(kTh) window_dkv_kernel(WinArgs a)
+__device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long block)
 {
     constexpr int MI = kBM / 8;
-    extern __shared__ __align__(16) float sm[];
     float *sk = sm, *sv = sk + kBM * (D + 4), *sq = sv + kBM * (D + 4), *sg = sq + kBN * (D + 4), *sp = sg + kBN * (D + 4);
     const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
     // sink blocks meet every later query: they come first in launch order
     const int units = a.B * a.Hkv;
-    const int tile = (int)(blockIdx.x / units), bh = (int)(blockIdx.x % units);
+    const int tile = (int)(block / units), bh = (int)(block % units);
     const int b = bh / a.Hkv, hk = bh - b * a.Hkv, G = a.H / a.Hkv;
     const int j0 = tile * kBM, j1 = min(a.Nk, j0 + kBM);
     const int first = win_first(a, b), kl = win_klen(a, b);
@@ -458,8 +500,9 @@ __global__ void __launch_bounds__(kTh) window_dkv_kernel(WinArgs a)
         const int h = hk * G + t / per, i0 = qr.x + t % per * kBN;
         arrived<0>();
         float s[MI][4], dp[MI][4];
-        scores<D, MI>(s, sk, sq, ty, tx);
-        scores<D, MI>(dp, sv, sg, ty, tx);
+        const Groups g = groups(0, min(4, (qr.y - i0 + 15) >> 4));
+        scores<D, MI>(s, sk, sq, ty, tx, g);
+        scores<D, MI>(dp, sv, sg, ty, tx, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int q = i0 + tx + 16 * j;
@@ -477,7 +520,7 @@ __global__ void __launch_bounds__(kTh) window_dkv_kernel(WinArgs a)
             }
         }
         __syncwarp();
-        accumulate<D, MI>(dv, sp, sg, ty, tx);
+        accumulate<D, MI>(dv, sp, sg, ty, tx, g);
         __syncthreads();
         queries(sg, a.G, a.lg, t + 1);
 #pragma unroll
@@ -485,7 +528,7 @@ __global__ void __launch_bounds__(kTh) window_dkv_kernel(WinArgs a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) sp[(ty + 8 * i) * kLdP + tx + 16 * j] = dp[i][j];
         __syncwarp();
-        accumulate<D, MI>(dk, sp, sq, ty, tx);
+        accumulate<D, MI>(dk, sp, sq, ty, tx, g);
         __syncthreads();
         queries(sq, a.Q, a.lq, t + 1);
     }
@@ -504,14 +547,38 @@ __global__ void __launch_bounds__(kTh) window_dkv_kernel(WinArgs a)
     }
 }
 
+// Both gradients in one grid, so that the end of one kind's blocks is filled by the other's (8 heads
+// x 1430, 360 blocks of each: as two grids the busiest SM had 1.48 and 1.33 times the mean's work).
+template <int D>
+__global__ void __launch_bounds__(kTh, D == 64 ? 3 : 2) window_bwd_kernel(WinArgs a)
+{
+    extern __shared__ __align__(16) float sm[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // D
+    const long long kv = (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM);
+    if (blockIdx.x < kv)
+        dkv_block<D>(a, sm, blockIdx.x);
+    else
+        dq_block<D>(a, sm, blockIdx.x - kv);
+}
+
+// early: launched while the kernel before it runs, which it waits for
 template <typename F>
-cudaError_t launch(F *kernel, long long grid, int smem, const WinArgs &a, cudaStream_t s)
+cudaError_t launch(F *kernel, long long grid, int smem, const WinArgs &a, cudaStream_t s, bool early = false)
 {
     if (grid < 1 || grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)grid, kTh, smem, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3(kTh);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &attr;
+    c.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, a);
 }
 
 template <int D>
@@ -528,11 +595,12 @@ cudaError_t forward(const WinArgs &a, cudaStream_t s)
 template <int D>
 cudaError_t backward(const WinArgs &a, cudaStream_t s)
 {
-    const int smem = (2 * kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4;
-    cudaError_t e = launch(window_dq_kernel<D>, (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM),
-                           (2 * kBM + kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s);
+    const long long rows = (long long)a.B * a.H * a.Nq;
+    cudaError_t e = launch(window_delta_kernel<D>, (rows + kTh / 32 - 1) / (kTh / 32), 0, a, s);
     if (e != cudaSuccess) return e;
-    return launch(window_dkv_kernel<D>, (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM), smem, a, s);
+    return launch(window_bwd_kernel<D>,
+                  (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM) + (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM),
+                  (2 * kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s, true);
 }
 
 }  // namespace
@@ -549,21 +617,12 @@ cudaError_t window_simt_backward(const WinArgs &a, cudaStream_t s)
 
 cudaError_t window_join(const WinArgs &a, cudaStream_t s)
 {
-    const long long rows = (long long)a.B * a.H * a.Nq;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)((rows + 3) / 4));
-    c.blockDim = dim3(128);
-    c.stream = s;
-    c.attrs = &early;
-    c.numAttrs = 1;
+    const long long blocks = ((long long)a.B * a.H * a.Nq + 3) / 4;
     if (a.is_bf16)
-        return a.d == 64 ? cudaLaunchKernelEx(&c, window_join_kernel<__nv_bfloat16, 64>, a)
-                         : cudaLaunchKernelEx(&c, window_join_kernel<__nv_bfloat16, 128>, a);
-    return a.d == 64 ? cudaLaunchKernelEx(&c, window_join_kernel<float, 64>, a)
-                     : cudaLaunchKernelEx(&c, window_join_kernel<float, 128>, a);
+        return a.d == 64 ? launch(window_join_kernel<__nv_bfloat16, 64>, blocks, 0, a, s, true)
+                         : launch(window_join_kernel<__nv_bfloat16, 128>, blocks, 0, a, s, true);
+    return a.d == 64 ? launch(window_join_kernel<float, 64>, blocks, 0, a, s, true)
+                     : launch(window_join_kernel<float, 128>, blocks, 0, a, s, true);
 }
 
 }  // namespace scope
