@@ -39,6 +39,7 @@ struct WinArgs {
 };
 
 constexpr int kWinUnbounded = 1 << 30;   // left / right of -1
+constexpr int kFewCluster = 6;           // few rows, bf16: up to as many shares join as a cluster
 
 struct WinRow {
     int s, lo, hi;

@@ -189,9 +189,11 @@ Plan plan_of(const scope_window_params &p)
     // ceil(tiles / shares) tiles and a fixed cost of about four 64-key tiles (start, store, join)
     r.splits = 1;
     const long long fixed = 256 / bn;
+    // few rows in bf16: a second kernel that joins costs as much again
+    const int joined = r.few && bf16 ? kFewCluster : kMaxSplits;
     long long best = -1;
     for (int n = 1; n <= kMaxSplits && (n == 1 || n * (128 / bn) <= key_tiles); ++n) {
-        const long long cost = ((items * n + slots - 1) / slots) * ((key_tiles + n - 1) / n + fixed);
+        const long long cost = ((items * n + slots - 1) / slots) * ((key_tiles + n - 1) / n + fixed) + (n > joined ? fixed : 0);
         if (best < 0 || cost < best) {
             best = cost;
             r.splits = n;

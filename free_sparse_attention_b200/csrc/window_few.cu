@@ -8,7 +8,7 @@
 // matrix instructions take a fifth of the time the loads need; a tcgen05 tile would be 7/8 idle
 // rows and pay the TMEM round trip.  Two blocks share an SM: 3 tiles of 8 KB per warp keep
 // 128 KB of loads in flight there.  The warps join through shared memory, and the shares of a unit,
-// up to 4, as one cluster through distributed shared memory, in order.
+// up to 6, as one cluster through distributed shared memory, in order.
 // Rows of a 16-key tile lie at 2 d bytes, 16-byte chunk c of row r at c ^ (r mod 8): the 8 rows
 // of an ldmatrix meet different banks.
 #include "window.cuh"
@@ -322,9 +322,9 @@ cudaError_t launch(const WinArgs &a, cudaStream_t s)
 template <int D>
 cudaError_t forward(const WinArgs &a, cudaStream_t s)
 {
-    // Up to 4 shares as a cluster (16 x 8 units of 2: 50 us against 53 with a second kernel); larger
-    // clusters leave slots of a GPC empty (40 units of 7: 56 us against 39).
-    if (a.splits > 1 && a.splits <= 4) return launch<D, true>(a, s);
+    // Up to 6 shares as a cluster (16 x 8 units of 2: 50 us against 53 with a second kernel; 40 units of
+    // 6: 39.5 against 41.5); larger ones leave slots of a GPC empty (40 units of 7: 60 us against 42).
+    if (a.splits > 1 && a.splits <= kFewCluster) return launch<D, true>(a, s);
     cudaError_t e = launch<D, false>(a, s);
     return e == cudaSuccess && a.splits > 1 ? window_join(a, s) : e;
 }

@@ -110,6 +110,14 @@ def test_few_rows_over_a_long_cache(Nq, H, Hkv, dtype):
         _run(p, dtype, backward=Nq == 3)
 
 
+@pytest.mark.parametrize("H", [200, 148, 98, 74, 59, 49, 30, 2])
+def test_few_rows_in_every_number_of_shares(H):
+    """Heads that leave each a different number of shares of its keys, one to six joined as a cluster and more by a
+    second kernel."""
+    p = _params("bf16", H=H, Hkv=H, Nq=1, Nk=3001, d=64, frame=50, left=60, right=0, sinks=3, q_first=3000)
+    _run(p, "bf16", backward=False)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_strided_tensors(dtype):
     """Slices of one [B, N, 3, H, d] buffer in, slices of another out, forward and backward."""
