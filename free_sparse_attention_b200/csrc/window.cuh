@@ -16,6 +16,49 @@ struct WinLayout {
     long long b, h, n;   // strides in elements; channels are contiguous
 };
 
+// dK, dV: a block owns a tile of keys and walks the queries that see it.  Tiles of sinks, which
+// every later query sees, and tiles under long windows are cut into shares of the walk, whose sums
+// lie in `part` as fp32 (dK, then dV of each share, `rows` keys a tile) until window_kv_join.
+// Items in order: sink tiles (tile, then unit, then share), then the others (unit, tile, share).
+struct KeyShares {
+    int units, tiles, sink;   // B * Hkv; key tiles; tiles of sinks among them
+    int of_sink, of_other;    // shares (1: written to dK, dV directly)
+    float *part;
+    __host__ __device__ long long sink_items() const { return (long long)units * sink * of_sink; }
+    __host__ __device__ long long items() const { return sink_items() + (long long)units * (tiles - sink) * of_other; }
+    // shares that are joined, and their place in `part`: sink items first
+    __host__ __device__ long long parts() const
+    {
+        return (of_sink > 1 ? sink_items() : 0) + (of_other > 1 ? items() - sink_items() : 0);
+    }
+    __host__ __device__ int shares(int tile) const { return tile < sink ? of_sink : of_other; }
+    __host__ __device__ long long item(int tile, int unit) const   // of share 0
+    {
+        return tile < sink ? ((long long)tile * units + unit) * of_sink
+                           : sink_items() + ((long long)unit * (tiles - sink) + tile - sink) * of_other;
+    }
+    __device__ __forceinline__ void at(int it, int &tile, int &unit, int &share) const   // items() < 2^31
+    {
+        const int sinks = units * sink * of_sink;
+        const bool is_sink = it < sinks;
+        const int of = is_sink ? of_sink : of_other, step = is_sink ? units : tiles - sink;
+        it -= is_sink ? 0 : sinks;
+        share = 0;
+        if (of > 1) {
+            share = it % of;
+            it /= of;
+        }
+        const int hi = it / step, lo = it - hi * step;
+        tile = is_sink ? hi : sink + lo;
+        unit = is_sink ? lo : hi;
+    }
+    // place of an item's sums (dK; dV behind it) for tiles of `rows` keys and d channels
+    __device__ float *sums(long long it, int rows, int d) const
+    {
+        return part + (it - (of_sink > 1 ? 0 : sink_items())) * 2 * rows * d;
+    }
+};
+
 struct WinArgs {
     const void *Q, *K, *V, *G;   // G: gradient of O (backward)
     void *O;                     // forward output; backward: the forward's output (read)
@@ -32,6 +75,7 @@ struct WinArgs {
     int pack;                    // query heads whose rows share a tile (few-row forms), or 1
     int splits;                  // key ranges of one row tile, joined afterwards (1: no join)
     float *part_o, *part_lse;    // [B*H*Nq, splits, d], [B*H*Nq, splits] (log2)
+    KeyShares kv;                // how dK, dV cut the query rows of a key tile
     float scale, scale_log2;     // 1/sqrt(d), log2(e)/sqrt(d)
     int32_t *status, *counter;
     int num_sms;
@@ -120,5 +164,6 @@ cudaError_t window_few_forward(const WinArgs &a, cudaStream_t s);   // bf16, pac
 cudaError_t window_simt_forward(const WinArgs &a, cudaStream_t s);    // fp32
 cudaError_t window_simt_backward(const WinArgs &a, cudaStream_t s);   // fp32
 cudaError_t window_join(const WinArgs &a, cudaStream_t s);
+cudaError_t window_kv_join(const WinArgs &a, int tile, cudaStream_t s);   // tile: keys a tile
 
 }  // namespace scope

@@ -202,8 +202,30 @@ Plan plan_of(const scope_window_params &p)
     return r;
 }
 
+// Shares of the key tiles in dK, dV: a share is at most half of what a mean SM has to walk, so that
+// the few tiles that all queries see do not end last, and no shorter than 16 column tiles.  Of the
+// shape alone.  (3 x 4 key heads x 4001, groups of 4, window 1024, 4 sinks: a tile of sinks walks 252
+// column tiles, the mean SM 211.)
+KeyShares shares_of(const scope_window_params &p)
+{
+    const long long tile = p.dtype == SCOPE_BF16 ? 128 : 32, G = p.H / p.Hkv;
+    const long long left = p.left < 0 ? kWinUnbounded : p.left, right = p.right < 0 ? kWinUnbounded : p.right;
+    KeyShares k{};
+    k.units = p.B * p.Hkv;
+    k.tiles = (int)((p.Nk + tile - 1) / tile);
+    k.sink = (int)std::min((long long)k.tiles, ((long long)p.sinks * p.frame + tile - 1) / tile);
+    // column tiles that one key tile walks, at most
+    const long long all = (p.Nq + 63) / 64, seen = std::min(all, (std::min((left + right + 1) * p.frame, 1ll << 24) + tile + 63) / 64 + 1);
+    const long long walk[2] = {G * all, G * seen};
+    const long long mean = k.units * (k.sink * walk[0] + (k.tiles - k.sink) * walk[1]) / kPlanSms;
+    const long long most = std::max(16ll, mean / 2);
+    k.of_sink = (int)((walk[0] + most - 1) / most);
+    k.of_other = (int)((walk[1] + most - 1) / most);
+    return k;
+}
+
 struct WinWs {
-    size_t part_o, part_lse, delta, nlse, total;
+    size_t part_o, part_lse, delta, nlse, part_kv, total;
 };
 
 WinWs ws_of(const scope_window_params &p)
@@ -218,7 +240,8 @@ WinWs ws_of(const scope_window_params &p)
     if (pl.splits > 1) o = align_up(o + sizeof(float) * rows * pl.splits);
     w.delta = kHeader;   // the backward pass has the partials' place to itself
     w.nlse = align_up(w.delta + sizeof(float) * rows);
-    w.total = std::max(o, p.dtype == SCOPE_BF16 ? align_up(w.nlse + sizeof(float) * rows) : w.nlse);
+    w.part_kv = p.dtype == SCOPE_BF16 ? align_up(w.nlse + sizeof(float) * rows) : w.nlse;
+    w.total = std::max(o, w.part_kv + sizeof(float) * 2 * (p.dtype == SCOPE_BF16 ? 128 : 32) * p.d * (size_t)shares_of(p).parts());
     return w;
 }
 
@@ -256,6 +279,8 @@ scope_status window_args(const scope_window_params &p, const scope_window_layout
     a.part_lse = reinterpret_cast<float *>(base + w.part_lse);
     a.delta = reinterpret_cast<float *>(base + w.delta);
     a.nlse = reinterpret_cast<float *>(base + w.nlse);
+    a.kv = shares_of(p);
+    a.kv.part = reinterpret_cast<float *>(base + w.part_kv);
     a.scale = (float)(1.0 / std::sqrt((double)p.d));
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)p.d));
     a.status = reinterpret_cast<int32_t *>(base);

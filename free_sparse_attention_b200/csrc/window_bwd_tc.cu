@@ -86,7 +86,9 @@ struct Item {
     WinRow a, z;           // dQ: limits of the first and last row
     WinTiles wt;           // dQ: key tiles
     int n;                 // dQ: their number, walked twice if a row sees few keys (below)
-    int c0, per, steps;    // dK, dV: first query tile and tiles per query head; steps in all
+    int c0, per, steps;    // dK, dV: first query tile and tiles per query head; steps of the share
+    int from;              // dK, dV: the share's first step
+    float *part;           // dK, dV: place of the share's sums, or NULL: dK, dV themselves
 };
 
 // D_i = dO_i . O_i carries the rounding of O to bf16, a share 2^-9 |O| |dO| that matters where a row
@@ -96,24 +98,17 @@ struct Item {
 // short by nature.
 constexpr int kFewKeys = 256;
 
-template <bool DKV, bool FEW>
+template <bool DKV, bool PLUS>
 __device__ __forceinline__ Item<DKV> item_of(const WinArgs &a, int it)
 {
     Item<DKV> x;
     const int n = DKV ? a.Nk : a.Nq, heads = DKV ? a.Hkv : a.H, tiles = (n + kBM - 1) / kBM;
-    int bh, tile;
+    int bh, tile, share = 0;
+    x.from = 0;
+    x.part = nullptr;
     if (DKV) {
         // sink tiles meet every later query: those of all heads first; then head by head
-        const int units = a.B * heads;
-        const int sink = (int)min((long long)tiles, ((long long)a.sinks * a.frame + kBM - 1) / kBM);
-        if (it < units * sink) {
-            tile = it / units;
-            bh = it % units;
-        } else {
-            it -= units * sink;
-            bh = it / (tiles - sink);
-            tile = sink + it % (tiles - sink);
-        }
+        a.kv.at(it, tile, bh, share);
     } else {
         bh = it / tiles;
         tile = tiles - 1 - it % tiles;
@@ -128,7 +123,13 @@ __device__ __forceinline__ Item<DKV> item_of(const WinArgs &a, int it)
         const int2 qr = win_queries(a, x.first, x.kl, a.Nq, x.r0, x.r0 + x.nrows);
         x.c0 = qr.x / kBN;
         x.per = qr.y > qr.x ? (qr.y + kBN - 1) / kBN - x.c0 : 0;
-        x.steps = x.per * (a.H / a.Hkv);
+        const int all = x.per * (a.H / a.Hkv), shares = PLUS ? a.kv.shares(tile) : 1;
+        x.steps = all;
+        if (PLUS && shares > 1) {
+            x.from = (int)((long long)all * share / shares);
+            x.steps = (int)((long long)all * (share + 1) / shares) - x.from;
+            x.part = a.kv.sums(it, kBM, a.d);
+        }
     } else {
         x.a = win_row(a, x.first + x.r0, x.kl);
         x.z = win_row(a, x.first + x.r0 + x.nrows - 1, x.kl);
@@ -136,7 +137,7 @@ __device__ __forceinline__ Item<DKV> item_of(const WinArgs &a, int it)
         x.n = x.wt.count();
         // the number of visible keys rises, stays and falls along the rows: least at an end
         const int least = min(x.a.s + x.a.hi - x.a.lo, x.z.s + x.z.hi - x.z.lo);
-        x.steps = FEW && least < kFewKeys ? 2 * x.n : x.n;
+        x.steps = PLUS && least < kFewKeys ? 2 * x.n : x.n;
     }
     return x;
 }
@@ -145,7 +146,10 @@ __device__ __forceinline__ Item<DKV> item_of(const WinArgs &a, int it)
 template <bool DKV>
 __device__ __forceinline__ int2 column_of(const WinArgs &a, const Item<DKV> &x, int t)
 {
-    if (DKV) return make_int2(x.h * (a.H / a.Hkv) + t / x.per, (x.c0 + t % x.per) * kBN);
+    if (DKV) {
+        t += x.from;   // 0 without shares
+        return make_int2(x.h * (a.H / a.Hkv) + t / x.per, (x.c0 + t % x.per) * kBN);
+    }
     return make_int2(x.h / (a.H / a.Hkv), x.wt.at(t < x.n ? t : t - x.n) * kBN);
 }
 
@@ -166,9 +170,10 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const float *src, bool i
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
 
-// FEW: some tile of the dQ pass may have rows that see few keys (the exact D costs every tile of
-// the pass 5 to 8 %, for the code it brings into the step loop, so it is left out where no row can).
-template <bool DKV, int D, bool FEW>
+// PLUS: some tile of the dQ pass may have rows that see few keys (the exact D costs every tile of
+// the pass 5 to 8 %, for the code it brings into the step loop, so it is left out where no row can),
+// or some tile of the dK, dV pass is cut into shares (2 to 3 %).
+template <bool DKV, int D, bool PLUS>
 __global__ void __launch_bounds__(kThreads, 1)
     window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmR1, const __grid_constant__ CUtensorMap tmR2,
                          const __grid_constant__ CUtensorMap tmC1, const __grid_constant__ CUtensorMap tmC2,
@@ -176,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using L = Smem<DKV, D>;
     using T = Cols<DKV, D>;
+    constexpr bool FEW = PLUS && !DKV, CUT = PLUS && DKV;
     constexpr int NB = D / 64, NS = L::kStages, NBUF = T::kBuf;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
                 const int it = next_item(item_k);
                 if (it < 0) break;
-                const Item<DKV> x = item_of<DKV, FEW>(a, it);
+                const Item<DKV> x = item_of<DKV, PLUS>(a, it);
                 if (x.steps == 0) continue;
                 int ok = 1;
                 if (lane == 0) {
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int it = ring[slot];
                 bar_arrive(BAR(item_empty) + 8u * (slot));
                 if (it < 0) break;
-                const Item<DKV> x = item_of<DKV, FEW>(a, it);
+                const Item<DKV> x = item_of<DKV, PLUS>(a, it);
                 const int steps = x.steps;
                 if (steps == 0) continue;
                 bool ok = true;
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
             const int it = next_item(item_k);
             if (it < 0) break;
-            const Item<DKV> x = item_of<DKV, FEW>(a, it);
+            const Item<DKV> x = item_of<DKV, PLUS>(a, it);
             const bool valid = row < x.nrows;
             auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
             // what the row sees: columns [0, s) and [lo, hi) (dQ) or [lo, hi) (dK, dV)
@@ -486,8 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // this warpgroup's steps: mine, mine + 2, ... below g + steps.  The column tile follows
             // without a division: position `at` of the query tiles of a head (dK, dV)
             int at = (int)(mine - g);
-            if constexpr (DKV)
+            if constexpr (DKV) {
+                if (CUT && x.per > 0) at = (at + x.from) % x.per;
                 while (at >= x.per && x.per > 0) at -= x.per;
+            }
             for (uint32_t from = g, walks = FEW && x.steps > x.n ? 2 : 1; walks > 0 && ok; --walks) {
             for (; ok && mine - from < (uint32_t)(DKV ? x.steps : x.n); mine += 2) {
                 const int j0 = (DKV ? (x.c0 + at) : x.wt.at((int)(mine - from))) * kBN;
@@ -639,6 +647,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 16; ++e) o[e] = 0.f;
                 }
                 if (!valid) continue;
+                if (CUT && x.part) {
+                    float *sum = x.part + odd * (kBM * D) + row * D + h * 16;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<float4 *>(sum + e) =
+                            make_float4(o[e] * scale, o[e + 1] * scale, o[e + 2] * scale, o[e + 3] * scale);
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 16; e += 8) {
                     uint32_t pk[4];
@@ -698,7 +714,7 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WinArgs a)
     }
 }
 
-template <bool DKV, int D, bool FEW>
+template <bool DKV, int D, bool PLUS>
 cudaError_t launch_pass(const WinArgs &a, cudaStream_t s)
 {
     CUtensorMap r1, r2, c1, c2;
@@ -708,14 +724,14 @@ cudaError_t launch_pass(const WinArgs &a, cudaStream_t s)
         !rows_map(&k, a.K, a.lk, a.B, a.Hkv, a.Nk, D, keys) || !rows_map(&v, a.V, a.lv, a.B, a.Hkv, a.Nk, D, keys))
         return cudaErrorInvalidValue;
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, window_bwd_tc_kernel<DKV, D, FEW>) != cudaSuccess || fa.numRegs != kLaunchRegs)
+    if (cudaFuncGetAttributes(&fa, window_bwd_tc_kernel<DKV, D, PLUS>) != cudaSuccess || fa.numRegs != kLaunchRegs)
         return cudaErrorInvalidDeviceFunction;
-    const long long items = DKV ? (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM) : (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM);
+    const long long items = DKV ? a.kv.items() : (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM);
     if (items > 0x7ffffff0ll) return cudaErrorInvalidConfiguration;
     const int smem = Smem<DKV, D>::kAlloc;
-    cudaError_t e = cudaFuncSetAttribute(window_bwd_tc_kernel<DKV, D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(window_bwd_tc_kernel<DKV, D, PLUS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    window_bwd_tc_kernel<DKV, D, FEW><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(r1, r2, c1, c2, a,
+    window_bwd_tc_kernel<DKV, D, PLUS><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(r1, r2, c1, c2, a,
                                                                                                            (int)items);
     return cudaGetLastError();
 }
@@ -735,7 +751,9 @@ cudaError_t backward(const WinArgs &a, cudaStream_t s)
         few = few || hi - lo + std::min(lo, (long long)a.sinks * a.frame) < kFewKeys;
     }
     if (e == cudaSuccess) e = few ? launch_pass<false, D, true>(a, s) : launch_pass<false, D, false>(a, s);
-    if (e == cudaSuccess) e = launch_pass<true, D, false>(a, s);
+    const bool cut = a.kv.parts() > 0;
+    if (e == cudaSuccess) e = cut ? launch_pass<true, D, true>(a, s) : launch_pass<true, D, false>(a, s);
+    if (e == cudaSuccess && cut) e = window_kv_join(a, kBM, s);
     return e;
 }
 

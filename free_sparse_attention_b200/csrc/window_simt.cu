@@ -364,6 +364,35 @@ __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a)
     if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
+// Joins the shares of the key tiles that were cut, in order: blockIdx.y is the tile, a thread 4
+// channels of dK (blockIdx.z = 0) or dV of one key.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) window_kv_join_kernel(WinArgs a, int rows)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tile = blockIdx.y + (a.kv.of_sink > 1 ? 0 : a.kv.sink), e = (int)threadIdx.x % (D / 4);
+    const long long r = (long long)blockIdx.x * (128 / (D / 4)) + threadIdx.x / (D / 4);   // unit, key of the tile
+    const int unit = (int)(r / rows), key = (int)(r % rows), j = tile * rows + key;
+    if (unit >= a.kv.units || j >= a.Nk) return;
+    const float *p = a.kv.sums(a.kv.item(tile, unit), rows, D) + (long long)blockIdx.z * rows * D + (long long)key * D + 4 * e;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = a.kv.shares(tile); s > 0; --s, p += 2ll * rows * D) {
+        const float4 v = load4(p);
+        x[0] += v.x;
+        x[1] += v.y;
+        x[2] += v.z;
+        x[3] += v.w;
+    }
+    const WinLayout lay = blockIdx.z ? a.ldv : a.ldk;
+    T *dst = static_cast<T *>(blockIdx.z ? a.dV : a.dK) + unit / a.Hkv * lay.b + unit % a.Hkv * lay.h + j * lay.n + 4 * e;
+    if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    } else {
+        store4(dst, make_float4(x[0], x[1], x[2], x[3]));
+    }
+}
+
 // D_i = dO_i . O_i, one warp per row.
 template <int D>
 __global__ void __launch_bounds__(kTh) window_delta_kernel(WinArgs a)
@@ -472,13 +501,15 @@ __device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long
     float *sk = sm, *sv = sk + kBM * (D + 4), *sq = sv + kBM * (D + 4), *sg = sq + kBN * (D + 4), *sp = sg + kBN * (D + 4);
     const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
     // sink blocks meet every later query: they come first in launch order
-    const int units = a.B * a.Hkv;
-    const int tile = (int)(block / units), bh = (int)(block % units);
+    int tile, bh, share;
+    a.kv.at((int)block, tile, bh, share);
+    const int shares = a.kv.shares(tile);
     const int b = bh / a.Hkv, hk = bh - b * a.Hkv, G = a.H / a.Hkv;
     const int j0 = tile * kBM, j1 = min(a.Nk, j0 + kBM);
     const int first = win_first(a, b), kl = win_klen(a, b);
     const int2 qr = win_queries(a, first, kl, a.Nq, j0, j1);
-    const int per = (qr.y - qr.x + kBN - 1) / kBN, nt = per * G;   // column tiles: per query head, in all
+    const int per = (qr.y - qr.x + kBN - 1) / kBN, all = per * G;   // column tiles: per query head, in all
+    const int t0 = (int)((long long)all * share / shares), nt = (int)((long long)all * (share + 1) / shares);
     const float *kb = static_cast<const float *>(a.K) + b * a.lk.b + hk * a.lk.h;
     const float *vb = static_cast<const float *>(a.V) + b * a.lv.b + hk * a.lv.h;
     auto queries = [&](float *dst, const void *tensor, const WinLayout &lay, int t) {
@@ -489,14 +520,14 @@ __device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long
     };
     load_tile<D, kBM>(sk, kb, [&](int r) -> const float * { return j0 + r < min(j1, kl) ? kb + (j0 + r) * a.lk.n : nullptr; });
     load_tile<D, kBM>(sv, vb, [&](int r) -> const float * { return j0 + r < min(j1, kl) ? vb + (j0 + r) * a.lv.n : nullptr; });
-    queries(sg, a.G, a.lg, 0);
-    queries(sq, a.Q, a.lq, 0);
+    queries(sg, a.G, a.lg, t0);
+    queries(sq, a.Q, a.lq, t0);
     uint64_t dk[MI][D / 32], dv[MI][D / 32];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) dk[i][e] = dv[i][e] = 0ull;
-    for (int t = 0; t < nt; ++t) {
+    for (int t = t0; t < nt; ++t) {
         const int h = hk * G + t / per, i0 = qr.x + t % per * kBN;
         arrived<0>();
         float s[MI][4], dp[MI][4];
@@ -538,6 +569,15 @@ __device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long
     for (int i = 0; i < MI; ++i) {
         const int j = j0 + ty + 8 * i;
         if (j >= j1) continue;
+        if (shares > 1) {
+            float *sum = a.kv.sums(block, kBM, D) + (ty + 8 * i) * D + 4 * tx;
+#pragma unroll
+            for (int jj = 0; jj < D / 64; ++jj) {
+                store_scaled(sum + 64 * jj, &dk[i][2 * jj], a.scale);
+                store_scaled(sum + kBM * D + 64 * jj, &dv[i][2 * jj], 1.f);
+            }
+            continue;
+        }
 #pragma unroll
         for (int jj = 0; jj < D / 64; ++jj) {
             const int c = 4 * tx + 64 * jj;
@@ -554,7 +594,7 @@ __global__ void __launch_bounds__(kTh, D == 64 ? 3 : 2) window_bwd_kernel(WinArg
 {
     extern __shared__ __align__(16) float sm[];
     asm volatile("griddepcontrol.wait;" ::: "memory");   // D
-    const long long kv = (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM);
+    const long long kv = a.kv.items();
     if (blockIdx.x < kv)
         dkv_block<D>(a, sm, blockIdx.x);
     else
@@ -598,9 +638,9 @@ cudaError_t backward(const WinArgs &a, cudaStream_t s)
     const long long rows = (long long)a.B * a.H * a.Nq;
     cudaError_t e = launch(window_delta_kernel<D>, (rows + kTh / 32 - 1) / (kTh / 32), 0, a, s);
     if (e != cudaSuccess) return e;
-    return launch(window_bwd_kernel<D>,
-                  (long long)a.B * a.Hkv * ((a.Nk + kBM - 1) / kBM) + (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM),
-                  (2 * kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s, true);
+    e = launch(window_bwd_kernel<D>, a.kv.items() + (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM),
+               (2 * kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s, true);
+    return e == cudaSuccess && a.kv.parts() > 0 ? window_kv_join(a, kBM, s) : e;
 }
 
 }  // namespace
@@ -613,6 +653,26 @@ cudaError_t window_simt_forward(const WinArgs &a, cudaStream_t s)
 cudaError_t window_simt_backward(const WinArgs &a, cudaStream_t s)
 {
     return a.d == 64 ? backward<64>(a, s) : backward<128>(a, s);
+}
+
+cudaError_t window_kv_join(const WinArgs &a, int tile, cudaStream_t s)
+{
+    const int from = a.kv.of_sink > 1 ? 0 : a.kv.sink, to = a.kv.of_other > 1 ? a.kv.tiles : a.kv.sink;
+    const int per = 128 / (a.d / 4);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(((long long)a.kv.units * tile + per - 1) / per), (unsigned)(to - from), 2);
+    c.blockDim = dim3(128);
+    c.stream = s;
+    c.attrs = &attr;
+    c.numAttrs = 1;
+    if (a.is_bf16)
+        return a.d == 64 ? cudaLaunchKernelEx(&c, window_kv_join_kernel<__nv_bfloat16, 64>, a, tile)
+                         : cudaLaunchKernelEx(&c, window_kv_join_kernel<__nv_bfloat16, 128>, a, tile);
+    return a.d == 64 ? cudaLaunchKernelEx(&c, window_kv_join_kernel<float, 64>, a, tile)
+                     : cudaLaunchKernelEx(&c, window_kv_join_kernel<float, 128>, a, tile);
 }
 
 cudaError_t window_join(const WinArgs &a, cudaStream_t s)

@@ -119,6 +119,19 @@ def test_few_rows_in_every_number_of_shares(H):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape,k_len", [
+    (dict(H=2, Hkv=1, Nq=1500, left=50, sinks=4), None),                              # only the sinks are cut
+    (dict(H=1, Nq=1300, left=-1, right=0, d=128), None),                              # no sinks, every tile is
+    (dict(B=2, H=4, Hkv=2, Nq=1111, frame=100, left=5, right=0, sinks=2, d=128), [1111, 150]),   # both
+    (dict(H=3, Hkv=1, Nq=900, Nk=400, frame=300, left=0, right=-1, sinks=1), [399]),
+])
+def test_gradients_of_keys_that_many_queries_see(shape, k_len, dtype):
+    """Key tiles whose walk over the queries is cut into shares: sinks, long windows, groups, short entries."""
+    p = _params(dtype, **shape)
+    _run(p, dtype, None, k_len)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_strided_tensors(dtype):
     """Slices of one [B, N, 3, H, d] buffer in, slices of another out, forward and backward."""
     p = _params(dtype, B=2, H=3, Nq=150, d=64, left=40, right=4, sinks=3)
