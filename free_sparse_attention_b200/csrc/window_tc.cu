@@ -47,6 +47,14 @@ struct __align__(8) Bars {
     uint64_t item_full[kRing], item_empty[kRing];
 };
 
+// One item of the forward pass.
+struct Item {
+    int b, h, hk, r0, nrows, split, kl, first;
+    WinRow a[2], z[2];   // limits of the first and last row of each Q tile (nrows > 128 q)
+    WinTiles all, q[2];  // key tiles of the item and of each Q tile
+    int t0, t1;          // the item's share of `all`
+};
+
 template <int D>
 struct Smem {
     static constexpr int kStages = D == 128 ? 5 : 8;   // K and V rings
@@ -57,17 +65,10 @@ struct Smem {
     static constexpr int kV = kK + kStages * kTile;
     static constexpr int kBars = kV + kStages * kTile;
     static constexpr int kMisc = kBars + (int)sizeof(Bars);
-    static constexpr int kAlloc = kMisc + 64 + 1024;
+    static constexpr int kItems = kMisc + 64;          // the ring's items
+    static constexpr int kAlloc = kItems + kRing * (int)sizeof(Item) + 1024;
     static_assert(kAlloc <= 232448, "shared memory budget");
     static_assert(kAlloc > 232448 / 2, "one CTA (and its 512 TMEM columns) per SM");
-};
-
-// One item of the forward pass.
-struct Item {
-    int b, h, hk, r0, nrows, split, kl, first;
-    WinRow a[2], z[2];   // limits of the first and last row of each Q tile (nrows > 128 q)
-    WinTiles all, q[2];  // key tiles of the item and of each Q tile
-    int t0, t1;          // the item's share of `all`
 };
 
 // Whether the rows with key tiles w see key tile k.
@@ -172,19 +173,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     // Scheduler: lane 0 of warp 8 takes item indices from the counter one item ahead and
-    // publishes them in a ring that every warp reads; -1 ends the work.
+    // publishes the items in a ring that every warp reads; -1 ends the work.
+    Item *const items_ring = reinterpret_cast<Item *>(sm + L::kItems);
     auto fetch = [&](uint32_t k) -> bool {
         const int slot = k % kRing;
         if (!wait1(BAR(item_empty) + 8u * (slot), ((k / kRing) & 1) ^ 1, W)) return false;
         const int it = atomicAdd(a.counter, 1);
+        if (it < n_items) items_ring[slot] = item_of(a, it, tiles);
         ring[slot] = it < n_items ? it : -1;
         bar_arrive(BAR(item_full) + 8u * (slot));
         return true;
     };
-    auto next_item = [&](uint32_t k) -> int {
+    auto next_item = [&](uint32_t k, Item &x) -> int {
         const int slot = k % kRing;
         if (!waitw(BAR(item_full) + 8u * (slot), (k / kRing) & 1, W)) return -1;
         const int it = ring[slot];
+        x = items_ring[slot];
         __syncwarp();
         if (lane == 0) bar_arrive(BAR(item_empty) + 8u * (slot));
         if (warp == 8 && it >= 0) {
@@ -204,9 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------------- Q and K loads
             uint32_t k_it = 0, q_it = 0;
             for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
-                const int it = next_item(item_k);
-                if (it < 0) break;
-                const Item x = item_of(a, it, tiles);
+                Item x;
+                if (next_item(item_k, x) < 0) break;
                 if (x.t0 == x.t1) continue;
                 int ok = 1;
                 if (lane == 0) {
@@ -247,9 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t v_it = 0, land = 0;
             bool landing = false;   // an edge tile's copy was issued and not yet waited for
             for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
-                const int it = next_item(item_k);
-                if (it < 0) break;
-                const Item x = item_of(a, it, tiles);
+                Item x;
+                if (next_item(item_k, x) < 0) break;
                 const WinRow za = x.a[0], zz = x.nrows > kBM ? x.z[1] : x.z[0];
                 int ok = 1;
                 for (int t = x.t0; t < x.t1 && ok; ++t) {
@@ -311,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int slot = item_k % kRing;
                     if (!wait1(BAR(item_full) + 8u * (slot), (item_k / kRing) & 1, W)) break;
                     const int it = ring[slot];
+                    const Item x = items_ring[slot];
                     bar_arrive(BAR(item_empty) + 8u * (slot));
                     if (it < 0) break;
-                    const Item x = item_of(a, it, tiles);
                     if (x.t0 == x.t1) continue;
                     const WinTiles mine = pick(q == 1, x.q);
                     bool ok = true;
@@ -391,14 +393,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s_par = 0, o_par = 0;   // parities of the next s_full / of the o_done before the item
         const float c = a.scale_log2;
         auto pv_parity = [&](int j) -> uint32_t { return ((o_par >> (j % NSB)) + (uint32_t)(j / NSB)) & 1u; };
-        for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
-            const int it = next_item(item_k);
-            if (it < 0) break;
-            const Item x = item_of(a, it, tiles);
-            if (q * kBM >= x.nrows) continue;
-            const int r = q * kBM + row;
+        // the item, and what this thread's row sees of it: taken while the last product of the item
+        // before it runs
+        const int r = q * kBM + row;
+        Item next;
+        WinRow next_lim;
+        uint32_t item_k = 0;
+        auto take = [&]() -> int {
+            const int it = next_item(item_k++, next);
+            if (it >= 0) next_lim = r < next.nrows ? win_row(a, next.first + r, next.kl) : WinRow{0, 0, 0};
+            return it;
+        };
+        int it = take();
+        while (it >= 0 && !warp_aborted(abort_flag)) {
+            const Item x = next;
+            const WinRow lim = next_lim;
+            if (q * kBM >= x.nrows) {
+                it = take();
+                continue;
+            }
             const bool valid = r < x.nrows;
-            const WinRow lim = valid ? win_row(a, x.first + r, x.kl) : WinRow{0, 0, 0};
             const WinTiles mine = pick(q == 1, x.q);
             const WinRow first_row = pick(q == 1, x.a), last_row = pick(q == 1, x.z);
             float m_run = -INFINITY, l = 0.f;
@@ -482,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++n;
             }
             if (!ok) break;
+            it = take();
             if (n > 0) {
                 if (!waitw(BAR(o_done) + 8u * (kMaxSB * (q) + ((n - 1) % NSB)), pv_parity(n - 1), W)) break;
 #pragma unroll
