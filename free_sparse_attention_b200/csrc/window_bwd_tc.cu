@@ -63,21 +63,6 @@ struct Cols {
     }
 };
 
-template <bool DKV, int D>
-struct Smem {
-    static constexpr int kStages = D == 128 ? (DKV ? 4 : 5) : 8;
-    static constexpr int kRows = kBM * D * 2, kTile = kBN * D * 2;
-    static constexpr int kR1 = 0, kR2 = kRows, kC = 2 * kRows;               // stage s: C1, C2
-    static constexpr int kLs = kC + kStages * 2 * kTile;                     // stage s: lse [64], D [64]
-    static constexpr int kSums = kLs;                                        // dQ: [2][128] row sums of dS
-    static constexpr int kBars = kLs + (DKV ? kStages * 2 * kBN * 4 : 2 * kBM * 4);
-    static constexpr int kMisc = kBars + (int)sizeof(Bars);
-    static constexpr int kAlloc = kMisc + 64 + 1024;
-    static_assert(kAlloc <= 232448, "shared memory budget");
-    static_assert(kAlloc > 232448 / 2, "one CTA (and its 512 TMEM columns) per SM");
-    static_assert(kStages <= kMaxStages, "ring depth");
-};
-
 // One item: 128 rows of one head, and its column tiles in order.
 template <bool DKV>
 struct Item {
@@ -89,6 +74,22 @@ struct Item {
     int c0, per, steps;    // dK, dV: first query tile and tiles per query head; steps of the share
     int from;              // dK, dV: the share's first step
     float *part;           // dK, dV: place of the share's sums, or NULL: dK, dV themselves
+};
+
+template <bool DKV, int D>
+struct Smem {
+    static constexpr int kStages = D == 128 ? (DKV ? 4 : 5) : 8;
+    static constexpr int kRows = kBM * D * 2, kTile = kBN * D * 2;
+    static constexpr int kR1 = 0, kR2 = kRows, kC = 2 * kRows;               // stage s: C1, C2
+    static constexpr int kLs = kC + kStages * 2 * kTile;                     // stage s: lse [64], D [64]
+    static constexpr int kSums = kLs;                                        // dQ: [2][128] row sums of dS
+    static constexpr int kBars = kLs + (DKV ? kStages * 2 * kBN * 4 : 2 * kBM * 4);
+    static constexpr int kMisc = kBars + (int)sizeof(Bars);
+    static constexpr int kItems = kMisc + 64;                                // the ring's items
+    static constexpr int kAlloc = kItems + kRing * (int)sizeof(Item<DKV>) + 1024;
+    static_assert(kAlloc <= 232448, "shared memory budget");
+    static_assert(kAlloc > 232448 / 2, "one CTA (and its 512 TMEM columns) per SM");
+    static_assert(kStages <= kMaxStages, "ring depth");
 };
 
 // D_i = dO_i . O_i carries the rounding of O to bf16, a share 2^-9 |O| |dO| that matters where a row
@@ -240,18 +241,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t out1 = tmem + T::kOut, out2 = out1 + D;   // dQ or dK; dV
-    auto fetch = [&](uint32_t k) -> bool {   // lane 0 of warp 8: the item scheduler
+    // lane 0 of warp 8 is the item scheduler: it decodes an item ahead, for all
+    Item<DKV> *const items_ring = reinterpret_cast<Item<DKV> *>(sm + L::kItems);
+    auto fetch = [&](uint32_t k) -> bool {
         const int slot = k % kRing;
         if (!wait1(BAR(item_empty) + 8u * (slot), ((k / kRing) & 1) ^ 1, W)) return false;
         const int it = atomicAdd(counter, 1);
+        if (it < n_items) items_ring[slot] = item_of<DKV, PLUS>(a, it);
         ring[slot] = it < n_items ? it : -1;
         bar_arrive(BAR(item_full) + 8u * (slot));
         return true;
     };
-    auto next_item = [&](uint32_t k) -> int {
+    auto next_item = [&](uint32_t k, Item<DKV> &x) -> int {
         const int slot = k % kRing;
         if (!waitw(BAR(item_full) + 8u * (slot), (k / kRing) & 1, W)) return -1;
         const int it = ring[slot];
+        x = items_ring[slot];
         __syncwarp();
         if (lane == 0) bar_arrive(BAR(item_empty) + 8u * (slot));
         if (warp == 8 && it >= 0) {
@@ -274,9 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r_it = 0, land = 0;
             bool landing = false;
             for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
-                const int it = next_item(item_k);
-                if (it < 0) break;
-                const Item<DKV> x = item_of<DKV, PLUS>(a, it);
+                Item<DKV> x;
+                if (next_item(item_k, x) < 0) break;
                 if (x.steps == 0) continue;
                 int ok = 1;
                 if (lane == 0) {
@@ -369,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot = item_k % kRing;
                 if (!wait1(BAR(item_full) + 8u * (slot), (item_k / kRing) & 1, W)) break;
                 const int it = ring[slot];
+                const Item<DKV> x = items_ring[slot];
                 bar_arrive(BAR(item_empty) + 8u * (slot));
                 if (it < 0) break;
-                const Item<DKV> x = item_of<DKV, PLUS>(a, it);
                 const int steps = x.steps;
                 if (steps == 0) continue;
                 bool ok = true;
@@ -447,27 +451,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the warpgroup's next step, with its buffers and their phases: S / dP buffer w, P / dS
         // buffer `odd`, column stage s
         uint32_t mine = odd, w = odd, s = odd, use = 0, pd_use = 0, s_use = 0, sums_use = 0;
-        for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
-            const int it = next_item(item_k);
-            if (it < 0) break;
-            const Item<DKV> x = item_of<DKV, PLUS>(a, it);
-            const bool valid = row < x.nrows;
-            auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
-            // what the row sees: columns [0, s) and [lo, hi) (dQ) or [lo, hi) (dK, dV)
-            WinRow lim{0, 0, 0};
-            float nlse = 0.f, ndelta = 0.f;
-            if (valid) {
-                if constexpr (DKV) {
-                    const int2 qr = win_queries(a, x.first, x.kl, a.Nq, x.r0 + row, x.r0 + row + 1);
-                    lim.lo = qr.x;
-                    lim.hi = qr.y;
-                } else {
-                    lim = win_row(a, x.first + x.r0 + row, x.kl);
-                    const long long ix = win_row_index(a, x.b, x.h, x.r0 + row);
-                    nlse = a.nlse[ix];
-                    ndelta = a.delta[ix];
-                }
+        auto below = [&](int e) { return e <= 0 ? 0ull : (e >= 64 ? ~0ull : (1ull << e) - 1ull); };
+        // the item, what this thread's row sees of it (columns [0, s) and [lo, hi) of dQ, [lo, hi) of
+        // dK, dV) and its -lse log2 e and -D: taken while the last products of the item before it run
+        Item<DKV> next;
+        WinRow next_lim{0, 0, 0};
+        float next_nlse = 0.f, next_ndelta = 0.f;
+        uint32_t item_k = 0;
+        auto take = [&]() -> int {
+            const int it = next_item(item_k++, next);
+            next_lim = WinRow{0, 0, 0};
+            if (it < 0 || row >= next.nrows) return it;
+            if constexpr (DKV) {
+                const int2 qr = win_queries(a, next.first, next.kl, a.Nq, next.r0 + row, next.r0 + row + 1);
+                next_lim.lo = qr.x;
+                next_lim.hi = qr.y;
+            } else {
+                next_lim = win_row(a, next.first + next.r0 + row, next.kl);
+                const long long ix = win_row_index(a, next.b, next.h, next.r0 + row);
+                next_nlse = a.nlse[ix];
+                next_ndelta = a.delta[ix];
             }
+            return it;
+        };
+        int it = take();
+        while (it >= 0 && !warp_aborted(abort_flag)) {
+            const Item<DKV> x = next;
+            const WinRow lim = next_lim;
+            const float nlse = next_nlse;
+            float ndelta = next_ndelta;
+            const bool valid = row < x.nrows;
             const unsigned long long c2 = f2pack(a.scale_log2, a.scale_log2), nlse2 = f2pack(nlse, nlse);
             unsigned long long ndelta2 = f2pack(ndelta, ndelta), sum2 = 0ull;
             const bool twice = FEW && x.steps > x.n;
@@ -623,6 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             g += x.steps;
             if (!ok) break;
+            it = take();
             // epilogue: dK by warpgroup 0 and dV by 1; of dQ, half the channels each
             if (x.steps > 0) {
                 if (!waitw(BAR(out_full), items & 1, W)) break;
