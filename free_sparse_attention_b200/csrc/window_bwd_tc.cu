@@ -35,7 +35,7 @@ constexpr int kMaxStages = 8, kMaxBuf = 3, kRing = 4;
 constexpr uint32_t kTmemCols = 512;
 
 struct __align__(8) Bars {
-    uint64_t r_full, r_empty, land, out_full, out_free, sums_full, sums_free;
+    uint64_t r_full, r_empty, land[2], out_full, out_free, sums_full, sums_free;
     uint64_t c_full[kMaxStages], c_empty[kMaxStages], ls_full[kMaxStages];
     uint64_t s_full[kMaxBuf], d_full[kMaxBuf], s_free[kMaxBuf], d_free[kMaxBuf];   // S and dP buffers
     uint64_t p_full[2], ds_full[2], pd_free[2], drain[3];                          // P and dS buffers
@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         misc[0] = 0;
         bar_init(&bars->r_full, 1);
         bar_init(&bars->r_empty, 2);
-        bar_init(&bars->land, 1);
+        bar_init(&bars->land[0], 1);
+        bar_init(&bars->land[1], 1);
         bar_init(&bars->out_full, 1);
         bar_init(&bars->out_free, 8);
         bar_init(&bars->sums_full, 8);
@@ -277,7 +278,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 8) {
             // ------------------------------------------------------------------ loads
             uint32_t r_it = 0, land = 0;
-            bool landing = false;
+            // dQ: a tile with key rows that no row of the item sees lands on a barrier of its own, and
+            // those rows are zeroed (0 x NaN would reach dQ) once the next tile's copy is on its way
+            constexpr uint32_t kNone = ~0u;
+            uint32_t edge = kNone, edge_next = kNone;   // its step; that of a second one when waits gave up
+            int edge_y = 0;                             // its first key
+            auto finish_edge = [&](const Item<DKV> &x, int ok) -> int {
+                if (edge == kNone || !ok) return ok;
+                if (!waitw(BAR(land) + 8u * (land & 1), (land >> 1) & 1, W)) return 0;
+                ++land;
+                for (int e = lane; e < kBN * NB * 8; e += 32) {
+                    const int r = e / (NB * 8), j = edge_y + r;
+                    if (!(j < x.a.s || (j >= x.a.lo && j < x.z.hi)))
+                        *reinterpret_cast<uint4 *>(sm + L::kC + edge % NS * 2 * L::kTile + (e / 8 % NB) * (kBN * 128) + r * 128 +
+                                                   (e % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(BAR(c_full) + 8u * (edge % NS));
+                edge = kNone;
+                return 1;
+            };
             for (uint32_t item_k = 0; !warp_aborted(abort_flag); ++item_k) {
                 Item<DKV> x;
                 if (next_item(item_k, x) < 0) break;
@@ -295,33 +316,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++r_it;
                     }
                 }
-                for (int t = 0; t < x.steps; ++t) {
+                // lane 0: waits for the step's stage and starts its copies, which arrive on `bar`
+                auto copy = [&](int2 col, uint32_t bar) -> int {
                     const int s = g % NS;
-                    const int2 col = column_of<DKV>(a, x, t);
-                    // dQ: key rows that no row of the item sees are zeroed (0 x NaN would reach dQ)
-                    const bool whole = DKV || col.y + kBN <= x.a.s || (col.y >= x.a.lo && col.y + kBN <= x.z.hi);
-                    if (lane == 0 && ok) {
-                        ok = wait1(BAR(c_empty) + 8u * (s), ((g / NS) & 1) ^ 1, W);
-                        if (ok) {
-                            const uint32_t bar = whole ? BAR(c_full) + 8u * (s) : BAR(land);
-                            bar_expect_tx(bar, 2 * L::kTile);
-                            const uint32_t dst = sbase + L::kC + s * 2 * L::kTile;
+                    if (!wait1(BAR(c_empty) + 8u * (s), ((g / NS) & 1) ^ 1, W)) return 0;
+                    bar_expect_tx(bar, 2 * L::kTile);
+                    const uint32_t dst = sbase + L::kC + s * 2 * L::kTile;
 #pragma unroll
-                            for (int k = 0; k < NB; ++k) {
-                                tma_rows(dst + k * (kBN * 128), &tmC1, k * 64, col.y, col.x, x.b, bar);
-                                tma_rows(dst + L::kTile + k * (kBN * 128), &tmC2, k * 64, col.y, col.x, x.b, bar);
-                            }
-                            if (!whole) {
-                                landing = true;
-                                ok = wait1(BAR(land), land & 1, W);
-                                landing = !ok;
-                            }
-                        }
+                    for (int k = 0; k < NB; ++k) {
+                        tma_rows(dst + k * (kBN * 128), &tmC1, k * 64, col.y, col.x, x.b, bar);
+                        tma_rows(dst + L::kTile + k * (kBN * 128), &tmC2, k * 64, col.y, col.x, x.b, bar);
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) break;
-                    __syncwarp();
-                    if constexpr (DKV) {
+                    return 1;
+                };
+                if constexpr (DKV) {
+                    for (int t = 0; t < x.steps; ++t, ++g) {
+                        const int s = g % NS;
+                        const int2 col = column_of<DKV>(a, x, t);
+                        if (lane == 0 && ok) ok = copy(col, BAR(c_full) + 8u * s);
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
+                        __syncwarp();
                         // -lse log2 e and -D of the columns beside the tile; the copies arrive on
                         // the barrier themselves
                         const uint32_t ls = sbase + L::kLs + s * (2 * kBN * 4) + lane * 4;
@@ -333,30 +348,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                             cp_async4(ls + kBN * 4 + 128 * k, a.delta + (in ? row + 32 * k : 0), in);
                         }
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(BAR(ls_full) + 8u * s) : "memory");
-                    } else {
+                    }
+                } else {
+                    for (int t = 0; t < x.steps && ok;) {
+                        // lane 0 alone, up to an edge tile, or one tile while an edge tile lands
+                        int whole = 1, y = 0;
+                        if (lane == 0)
+                            do {
+                                const int2 col = column_of<DKV>(a, x, t);
+                                y = col.y;
+                                whole = y + kBN <= x.a.s || (y >= x.a.lo && y + kBN <= x.z.hi);
+                                ok = copy(col, whole ? BAR(c_full) + 8u * (g % NS)
+                                                     : BAR(land) + 8u * ((land + (edge != kNone ? 1 : 0)) & 1));
+                                if (!ok) break;
+                                ++g;
+                                ++t;
+                            } while (whole && edge == kNone && t < x.steps);
+                        g = __shfl_sync(0xffffffffu, g, 0);
+                        t = __shfl_sync(0xffffffffu, t, 0);
+                        y = __shfl_sync(0xffffffffu, y, 0);
+                        whole = __shfl_sync(0xffffffffu, whole, 0);
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
+                        ok = finish_edge(x, ok);
                         if (!whole) {
-                            ++land;
-                            for (int e = lane; e < kBN * NB * 8; e += 32) {
-                                const int r = e / (NB * 8), j = col.y + r;
-                                if (!(j < x.a.s || (j >= x.a.lo && j < x.z.hi)))
-                                    *reinterpret_cast<uint4 *>(sm + L::kC + s * 2 * L::kTile + (e / 8 % NB) * (kBN * 128) +
-                                                               r * 128 + (e % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            }
-                            fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) bar_arrive(BAR(c_full) + 8u * (s));
+                            (ok ? edge : edge_next) = g - 1;
+                            edge_y = y;
                         }
                     }
-                    ++g;
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
+                if constexpr (!DKV) ok = finish_edge(x, ok);
                 if (!ok) break;
             }
             asm volatile("cp.async.wait_all;\n" ::: "memory");
             if (lane == 0) {   // copies already issued land before the CTA exits
                 for (uint32_t v = g > (uint32_t)NS ? g - NS : 0; v < g; ++v)
-                    drain_wait(BAR(c_full) + 8u * (v % NS), (v / NS) & 1, W.limit_ns);
-                if (landing) drain_wait(BAR(land), land & 1, W.limit_ns);
+                    if (v != edge && v != edge_next) drain_wait(BAR(c_full) + 8u * (v % NS), (v / NS) & 1, W.limit_ns);
+                for (uint32_t v = land; v < land + (edge != kNone) + (edge_next != kNone); ++v)
+                    drain_wait(BAR(land) + 8u * (v & 1), (v >> 1) & 1, W.limit_ns);
                 if (r_it > 0) drain_wait(BAR(r_full), (r_it - 1) & 1, W.limit_ns);
             }
             __syncwarp();
