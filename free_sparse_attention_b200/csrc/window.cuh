@@ -158,7 +158,7 @@ __device__ __forceinline__ long long win_row_index(const WinArgs &a, int b, int 
 }
 
 // Launchers (enqueue only).
-cudaError_t window_tc_forward(const WinArgs &a, cudaStream_t s);    // bf16
+cudaError_t window_tc_forward(const WinArgs &a, cudaStream_t s);    // bf16; clears the header itself
 cudaError_t window_tc_backward(const WinArgs &a, cudaStream_t s);   // bf16; clears the header itself
 cudaError_t window_few_forward(const WinArgs &a, cudaStream_t s);   // bf16, pack * Nq <= 16
 cudaError_t window_simt_forward(const WinArgs &a, cudaStream_t s);    // fp32

@@ -387,13 +387,7 @@ scope_status scope_window_attention(const scope_window_params *p, const scope_wi
     a.O = O;
     a.lse = lse;
     if (a.is_bf16 && plan_of(*p).few) return cuda_status(window_few_forward(a, s));   // joins its shares itself
-    cudaError_t e = cudaSuccess;
-    if (!a.is_bf16) {
-        e = window_simt_forward(a, s);
-    } else {
-        e = cudaMemsetAsync(ws, 0, kHeader, s);
-        if (e == cudaSuccess) e = window_tc_forward(a, s);
-    }
+    cudaError_t e = a.is_bf16 ? window_tc_forward(a, s) : window_simt_forward(a, s);
     if (e == cudaSuccess && a.splits > 1) e = window_join(a, s);
     return cuda_status(e);
 }

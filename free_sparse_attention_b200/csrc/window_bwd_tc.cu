@@ -268,6 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return it;
     };
+    // launched while the kernel before it ends, which it needs whole (D, the counters)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 8 && lane == 0) fetch(0);
 
     // Every role counts the CTA's steps in g: step g uses S / dP buffer g % NBUF, P / dS buffer
@@ -734,6 +737,7 @@ __global__ void __launch_bounds__(256) window_delta_kernel(WinArgs a)
         *a.status = 0;
         a.counter[0] = a.counter[1] = 0;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long row = (long long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR, rows = (long long)a.B * a.H * a.Nq;
     const int g = threadIdx.x % TPR;
     float s = 0.f;
@@ -775,9 +779,17 @@ cudaError_t launch_pass(const WinArgs &a, cudaStream_t s)
     const int smem = Smem<DKV, D>::kAlloc;
     cudaError_t e = cudaFuncSetAttribute(window_bwd_tc_kernel<DKV, D, PLUS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    window_bwd_tc_kernel<DKV, D, PLUS><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(r1, r2, c1, c2, a,
-                                                                                                           (int)items);
-    return cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(items < a.num_sms ? items : a.num_sms));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, window_bwd_tc_kernel<DKV, D, PLUS>, r1, r2, c1, c2, a, (int)items);
 }
 
 template <int D>

@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         misc[0] = 0;
+        if (!a.counter && blockIdx.x == 0) *a.status = 0;
         bar_init(&bars->q_full, 1);
         bar_init(&bars->q_empty, 2);
         bar_init(&bars->v_land, 1);
@@ -172,13 +173,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // Scheduler: lane 0 of warp 8 takes item indices from the counter one item ahead and
+    // Scheduler: lane 0 of warp 8 takes item indices from the counter (or, where there are no more
+    // items than CTAs, which then do without one, its CTA's) one item ahead and
     // publishes the items in a ring that every warp reads; -1 ends the work.
     Item *const items_ring = reinterpret_cast<Item *>(sm + L::kItems);
     auto fetch = [&](uint32_t k) -> bool {
         const int slot = k % kRing;
         if (!wait1(BAR(item_empty) + 8u * (slot), ((k / kRing) & 1) ^ 1, W)) return false;
-        const int it = atomicAdd(a.counter, 1);
+        const int it = a.counter ? atomicAdd(a.counter, 1) : (k == 0 ? (int)blockIdx.x : n_items);
         if (it < n_items) items_ring[slot] = item_of(a, it, tiles);
         ring[slot] = it < n_items ? it : -1;
         bar_arrive(BAR(item_full) + 8u * (slot));
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_forward(const WinArgs &a, cudaStream_t s)
+cudaError_t launch_forward(WinArgs a, cudaStream_t s)
 {
     CUtensorMap tq, tk, tv;
     if (!rows_map(&tq, a.Q, a.lq, a.B, a.H, a.Nq, D, kBM) || !rows_map(&tk, a.K, a.lk, a.B, a.Hkv, a.Nk, D, kBN) ||
@@ -571,6 +573,10 @@ cudaError_t launch_forward(const WinArgs &a, cudaStream_t s)
     const int smem = Smem<D>::kAlloc;
     cudaError_t e = cudaFuncSetAttribute(window_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    if (items <= a.num_sms)
+        a.counter = nullptr;   // nothing to clear first (some 2 us of a call)
+    else if ((e = cudaMemsetAsync(a.status, 0, (char *)(a.counter + 1) - (char *)a.status, s)) != cudaSuccess)
+        return e;
     window_tc_kernel<D><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(tq, tk, tv, a, (int)items);
     return cudaGetLastError();
 }
