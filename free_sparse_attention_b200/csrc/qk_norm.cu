@@ -106,6 +106,20 @@ __device__ __forceinline__ Place place_of(const NormArgs &a, int which, long lon
     return p;
 }
 
+// Backward: the token runs times the heads of q (or k), head after head, are cut evenly over the
+// blocks.  The place at position `pos` of a block's share, which ends at `end`: heads of one token
+// run, no more than 32 of them.
+__device__ __forceinline__ Place span_of(const NormArgs &a, int which, int pos, int end)
+{
+    const int heads = which ? a.Hkv : a.H, run = pos / heads;
+    Place p;
+    p.h0 = pos - run * heads;
+    p.h1 = min(min(heads, p.h0 + 32), p.h0 + end - pos);
+    p.b = run / a.tiles;
+    p.tile = run - p.b * a.tiles;
+    return p;
+}
+
 // The rows of a thread's places, in order, streamed through a ring of its own in shared memory
 // (cp.async; no thread reads another's slots): STAGES - 1 rows of X (and G) are in flight
 // whatever the registers hold, across the ends of places too.
@@ -115,17 +129,15 @@ struct Feed {
     static constexpr int kSmem = STAGES * (GRAD ? 2 : 1) * kThreads * BYTES;
     const NormArgs &a;
     const NormTensor &x;
-    const int which, step;
-    const long long places;
-    long long it;          // place of the next row to load
-    int h, h1;             // its head, and the end of the place's heads
+    const int which, end;
+    int pos;               // of the next row to load, its head, and the end of the place's heads
+    int h, h1;
     const T *src, *grd;
     T *slots;              // slot s of X at s * kThreads * 8, of G behind the STAGES slots of X
     int fill;
 
-    __device__ __forceinline__ Feed(const NormArgs &args, int w, int first, int blocks, void *smem)
-        : a(args), x(w ? args.k : args.q), which(w), step(blocks),
-          places((long long)args.B * args.tiles * (w ? args.chunks_k : args.chunks_q)), it(first - blocks), h(0), h1(0),
+    __device__ __forceinline__ Feed(const NormArgs &args, int w, int from, int to, void *smem)
+        : a(args), x(w ? args.k : args.q), which(w), end(to), pos(from), h(0), h1(0),
           slots(static_cast<T *>(smem) + threadIdx.x * 8), fill(0)
     {
 #pragma unroll
@@ -136,23 +148,21 @@ struct Feed {
 
     __device__ __forceinline__ void next()
     {
-        if (h == h1 && it < places) {
-            it += step;
-            if (it < places) {
-                const Place p = place_of(a, which, it);
+        if (pos < end) {
+            if (h == h1) {
+                const Place p = span_of(a, which, pos, end);
                 const int n = min(p.tile * ROWS + (int)threadIdx.x / TPR, a.N - 1), c = 8 * (threadIdx.x % TPR);
                 h = p.h0;
                 h1 = p.h1;
                 src = static_cast<const T *>(x.X) + p.b * x.lx.b + n * x.lx.n + h * x.lx.h + c;
                 if (GRAD) grd = static_cast<const T *>(x.G) + p.b * x.lg.b + n * x.lg.n + h * x.lg.h + c;
             }
-        }
-        if (it < places) {
 #pragma unroll
             for (int i = 0; i < BYTES / 16; ++i) {
                 copy16(slot(fill, 0) + i * (16 / sizeof(T)), src + i * (16 / sizeof(T)));
                 if (GRAD) copy16(slot(fill, 1) + i * (16 / sizeof(T)), grd + i * (16 / sizeof(T)));
             }
+            ++pos;
             ++h;
             src += x.lx.h;
             if (GRAD) grd += x.lg.h;
@@ -233,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks<T>) qk_norm_kernel(NormAr
 }
 
 // Backward.  A thread sums its weight gradients over its rows (one sum per place, added to the
-// thread's total, so that no sum runs over more than a chunk of heads before it joins the next
+// thread's total, so that no sum runs over more than 32 heads before it joins the next
 // level), the block adds its token rows up in shared memory and writes one partial, and
 // qk_norm_dw_kernel adds the partials in block order.
 template <typename T, int D>
@@ -242,9 +252,12 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks<T>) qk_norm_bwd_kernel(No
     constexpr int TPR = D / 8, ROWS = kThreads / TPR, STAGES = kBwdStages<T>;
     extern __shared__ __align__(16) unsigned char smem[];
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int which = blockIdx.x >= a.blocks_q, first = which ? blockIdx.x - a.blocks_q : blockIdx.x,
               blocks = which ? gridDim.x - a.blocks_q : a.blocks_q;
-    Feed<T, D, true, STAGES> feed(a, which, first, blocks, smem);
+    const long long rows = (long long)a.B * a.tiles * (which ? a.Hkv : a.H);
+    const int from = (int)(rows * first / blocks), to = (int)(rows * (first + 1) / blocks);
+    Feed<T, D, true, STAGES> feed(a, which, from, to, smem);
     const NormTensor &x = which ? a.k : a.q;
     const int g = threadIdx.x % TPR;
     float dw[8], w[8];
@@ -254,8 +267,9 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks<T>) qk_norm_bwd_kernel(No
         w[e] = x.w ? x.w[8 * g + e] : 1.f;
     }
     int take = 0;
-    for (long long it = first; it < feed.places; it += blocks) {
-        const Place pl = place_of(a, which, it);
+    for (int pos = from; pos < to;) {
+        const Place pl = span_of(a, which, pos, to);
+        pos += pl.h1 - pl.h0;
         const int n = pl.tile * ROWS + threadIdx.x / TPR;
         const bool in = n < a.N;
         T *dst = static_cast<T *>(x.Y) + pl.b * x.ly.b + n * x.ly.n + pl.h0 * x.ly.h + 8 * g;
@@ -315,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks<T>) qk_norm_bwd_kernel(No
 __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(NormArgs a, int blocks, int D)
 {
     __shared__ float red[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the partials are written
     const int which = blockIdx.x / (D / 32), c = (blockIdx.x % (D / 32)) * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
     const int first = which ? a.blocks_q : 0, last = which ? blocks : a.blocks_q;
     float s = 0.f;
@@ -359,10 +374,10 @@ template <typename T, int D>
 cudaError_t backward(NormArgs a, int num_sms, cudaStream_t s)
 {
     const int per_sm = kBwdBlocks<T>, sms = std::min(num_sms, kNormMaxBlocks / per_sm);
-    plan(a, sms);
-    // blocks in proportion to the rows of q and of k, at least one each
-    const long long places = (long long)a.B * a.tiles * (a.chunks_q + a.chunks_k);
-    const int grid = (int)std::min<long long>(places, (long long)sms * per_sm);
+    a.tiles = (a.N + kThreads / (D / 8) - 1) / (kThreads / (D / 8));
+    // blocks in proportion to the rows of q and of k, at least one each, of 4 heads or more
+    const long long rows = (long long)a.B * a.tiles * (a.H + (a.k.X ? a.Hkv : 0));
+    const int grid = (int)std::max<long long>(a.k.X ? 2 : 1, std::min<long long>(rows / 4, (long long)sms * per_sm));
     a.blocks_q = grid;
     if (a.k.X) a.blocks_q = std::min(std::max(1, (int)((long long)grid * a.H / (a.H + a.Hkv))), grid - 1);
     const int smem = Feed<T, D, true, kBwdStages<T>>::kSmem;
@@ -370,8 +385,16 @@ cudaError_t backward(NormArgs a, int num_sms, cudaStream_t s)
     if (e != cudaSuccess) return e;
     qk_norm_bwd_kernel<T, D><<<grid, kThreads, smem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    qk_norm_dw_kernel<<<2 * (D / 32), 1024, 0, s>>>(a, grid, D);
-    return cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(2 * (D / 32));
+    c.blockDim = dim3(1024);
+    c.stream = s;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, qk_norm_dw_kernel, a, grid, D);
 }
 
 }  // namespace
