@@ -19,6 +19,8 @@
 // own, and every operand has its own barrier (dV starts on P while dS is computed).  Only dK, dV
 // at d = 128 has no such room (2 x 128 columns of results): there P and dS replace S and dP.
 // P and dS are rounded to bf16 once, as operands; everything summed is fp32.
+// Measured (B200): 48 heads x 17550, d 64, frames of 1350, one to either side and the first: dQ 2.10 ms =
+// 766 TFLOP/s, dK dV 2.85 ms = 755; 3 x 16 heads of 4 key heads x 4001, d 128, window 1024: 184 and 222 us.
 #include "window_tc.cuh"
 
 #include <algorithm>

@@ -16,6 +16,10 @@
 // TMEM: NSB buffers of S per Q tile (64 fp32 columns; P as bf16 pairs over the first 32 columns
 // of its own buffer) and two O tiles.  S(n + NSB) follows P V(n), which frees its buffer.
 // Only tiles that some row sees in part pay for the mask (one 64-bit word per row and tile).
+// A step of 256 rows x 64 keys is bound by the chain S -> softmax -> P -> P V of either Q tile, about
+// 2100 cycles at d 128 against 1024 of exponentials and 1280 of products.  Measured (B200): 40 heads x
+// 32760, d 128, frames of 1560, two to either side and the first: 5.4 ms cold = 1080 TFLOP/s, 6.2 ms in a
+// long run under the power limit; 48 heads x 17550, d 64: 1.78 ms.
 #include "window_tc.cuh"
 
 namespace scope {
