@@ -16,6 +16,7 @@
 // backward of 96 heads x 17550, d 64: 111 to 122 us = 5.3 to 5.8 TB/s, bound by instruction issue
 // (79 %) before the memory.
 #include "qk_norm.cuh"
+#include "early.cuh"
 
 #include <algorithm>
 
@@ -198,6 +199,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, kFwdBlocks<T>) qk_norm_kernel(NormArgs a)
 {
     constexpr int TPR = D / 8, M = kBatch<T>;
+    early_next();
+    early_wait();
     const int which = blockIdx.x >= a.blocks_q;
     const Place pl = place_of(a, which, which ? blockIdx.x - a.blocks_q : blockIdx.x);
     const int g = threadIdx.x % TPR, n = pl.tile * (kThreads / TPR) + threadIdx.x / TPR;
@@ -252,8 +255,9 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks<T>) qk_norm_bwd_kernel(No
 {
     constexpr int TPR = D / 8, ROWS = kThreads / TPR, STAGES = kBwdStages<T>;
     extern __shared__ __align__(16) unsigned char smem[];
+    early_next();
+    early_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int which = blockIdx.x >= a.blocks_q, first = which ? blockIdx.x - a.blocks_q : blockIdx.x,
               blocks = which ? gridDim.x - a.blocks_q : a.blocks_q;
     const long long rows = (long long)a.B * a.tiles * (which ? a.Hkv : a.H);
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks<T>) qk_norm_bwd_kernel(No
 __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(NormArgs a, int blocks, int D)
 {
     __shared__ float red[32][33];
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the partials are written
+    early_wait();
     const int which = blockIdx.x / (D / 32), c = (blockIdx.x % (D / 32)) * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
     const int first = which ? a.blocks_q : 0, last = which ? blocks : a.blocks_q;
     float s = 0.f;
@@ -367,8 +371,7 @@ cudaError_t forward(NormArgs a, int num_sms, cudaStream_t s)
     const long long runs = (long long)a.B * a.tiles, grid = runs * (a.chunks_q + a.chunks_k);
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     a.blocks_q = (int)(runs * a.chunks_q);
-    qk_norm_kernel<T, D><<<(unsigned)grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(qk_norm_kernel<T, D>, dim3((unsigned)grid), kThreads, 0, s, 1, a);
 }
 
 template <typename T, int D>
@@ -384,18 +387,8 @@ cudaError_t backward(NormArgs a, int num_sms, cudaStream_t s)
     const int smem = Feed<T, D, true, kBwdStages<T>>::kSmem;
     cudaError_t e = cudaFuncSetAttribute(qk_norm_bwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    qk_norm_bwd_kernel<T, D><<<grid, kThreads, smem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3(2 * (D / 32));
-    c.blockDim = dim3(1024);
-    c.stream = s;
-    c.attrs = &early;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, qk_norm_dw_kernel, a, grid, D);
+    if ((e = launch_early(qk_norm_bwd_kernel<T, D>, dim3(grid), kThreads, smem, s, 1, a)) != cudaSuccess) return e;
+    return launch_early(qk_norm_dw_kernel, dim3(2 * (D / 32)), 1024, 0, s, 1, a, grid, D);
 }
 
 }  // namespace

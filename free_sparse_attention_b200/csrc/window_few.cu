@@ -80,8 +80,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) window_few_kernel(WinArgs a
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float sm_m[kFewWarps][16], sm_l[kFewWarps][16], sm_bm[16], sm_bl[16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tg = lane & 3, tr = lane >> 2;
+    early_next();
+    early_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;   // this path has no device conditions
-    if (!CLUSTER) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
     const int groups = a.H / a.pack, b = unit / groups, h0 = (unit - b * groups) * a.pack, hk = h0 / (a.H / a.Hkv);
     const int rows = a.pack * a.Nq;
@@ -306,18 +307,8 @@ cudaError_t launch(const WinArgs &a, cudaStream_t s)
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(window_few_kernel<D, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute shares{};
-    shares.id = cudaLaunchAttributeClusterDimension;
-    shares.val.clusterDim.x = (unsigned)a.splits;
-    shares.val.clusterDim.y = shares.val.clusterDim.z = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)grid);
-    c.blockDim = dim3(kFewWarps * 32);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    c.attrs = &shares;
-    c.numAttrs = CLUSTER ? 1 : 0;
-    return cudaLaunchKernelEx(&c, window_few_kernel<D, CLUSTER>, a);
+    return launch_early(window_few_kernel<D, CLUSTER>, dim3((unsigned)grid), kFewWarps * 32, smem, s,
+                        CLUSTER ? (unsigned)a.splits : 1u, a);
 }
 
 template <int D>

@@ -213,8 +213,9 @@ __global__ void __launch_bounds__(kTh, D == 64 ? 4 : 3) window_fwd_kernel(WinArg
 {
     constexpr int MI = BM / 8;
     extern __shared__ __align__(16) float sm[];
+    early_next();
+    early_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;   // this path has no device conditions
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float *sq = sm, *sc = sq + BM * (D + 4), *sp = sc + kBN * (D + 4);   // sc: K, then V of a tile
     const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
     const int rows = a.pack * a.Nq, tiles = (rows + BM - 1) / BM;
@@ -332,9 +333,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a)
 {
     constexpr int PER = D / 32;
-    // launched while the shares still run (their blocks give the signal); nothing is read before
-    // they are complete
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    early_next();
+    early_wait();
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= (long long)a.B * a.H * a.Nq) return;
@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(128) window_join_kernel(WinArgs a)
 template <typename T, int D>
 __global__ void __launch_bounds__(128) window_kv_join_kernel(WinArgs a, int rows)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    early_next();
+    early_wait();
     const int tile = blockIdx.y + (a.kv.of_sink > 1 ? 0 : a.kv.sink), e = (int)threadIdx.x % (D / 4);
     const long long r = (long long)blockIdx.x * (128 / (D / 4)) + threadIdx.x / (D / 4);   // unit, key of the tile
     const int unit = (int)(r / rows), key = (int)(r % rows), j = tile * rows + key;
@@ -397,8 +398,9 @@ __global__ void __launch_bounds__(128) window_kv_join_kernel(WinArgs a, int rows
 template <int D>
 __global__ void __launch_bounds__(kTh) window_delta_kernel(WinArgs a)
 {
+    early_next();
+    early_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long row = (long long)blockIdx.x * (kTh / 32) + (threadIdx.x >> 5);
     if (row >= (long long)a.B * a.H * a.Nq) return;
     const int i = (int)(row % a.Nq), h = (int)(row / a.Nq % a.H), b = (int)(row / a.Nq / a.H), c = 4 * (threadIdx.x & 31);
@@ -593,7 +595,8 @@ template <int D>
 __global__ void __launch_bounds__(kTh, D == 64 ? 3 : 2) window_bwd_kernel(WinArgs a)
 {
     extern __shared__ __align__(16) float sm[];
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // D
+    early_next();
+    early_wait();
     // dQ's blocks first: those of dK, dV are cut finer (410 us against 458 the other way round, 8 heads x 1430, d 128)
     const long long q = (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM);
     if (blockIdx.x < q)
@@ -602,26 +605,15 @@ __global__ void __launch_bounds__(kTh, D == 64 ? 3 : 2) window_bwd_kernel(WinArg
         dkv_block<D>(a, sm, blockIdx.x - q);
 }
 
-// early: launched while the kernel before it runs, which it waits for
 template <typename F>
-cudaError_t launch(F *kernel, long long grid, int smem, const WinArgs &a, cudaStream_t s, bool early = false)
+cudaError_t launch(F *kernel, long long grid, int smem, const WinArgs &a, cudaStream_t s)
 {
     if (grid < 1 || grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)grid);
-    c.blockDim = dim3(kTh);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    c.attrs = &attr;
-    c.numAttrs = early ? 1 : 0;
-    return cudaLaunchKernelEx(&c, kernel, a);
+    return launch_early(kernel, dim3((unsigned)grid), kTh, smem, s, 1, a);
 }
 
 template <int D>
@@ -642,7 +634,7 @@ cudaError_t backward(const WinArgs &a, cudaStream_t s)
     cudaError_t e = launch(window_delta_kernel<D>, (rows + kTh / 32 - 1) / (kTh / 32), 0, a, s);
     if (e != cudaSuccess) return e;
     e = launch(window_bwd_kernel<D>, a.kv.items() + (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM),
-               (2 * kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s, true);
+               (2 * kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s);
     return e == cudaSuccess && a.kv.parts() > 0 ? window_kv_join(a, kBM, s) : e;
 }
 
@@ -662,30 +654,22 @@ cudaError_t window_kv_join(const WinArgs &a, int tile, cudaStream_t s)
 {
     const int from = a.kv.of_sink > 1 ? 0 : a.kv.sink, to = a.kv.of_other > 1 ? a.kv.tiles : a.kv.sink;
     const int per = 128 / (a.d / 4);
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)(((long long)a.kv.units * tile + per - 1) / per), (unsigned)(to - from), 2);
-    c.blockDim = dim3(128);
-    c.stream = s;
-    c.attrs = &attr;
-    c.numAttrs = 1;
+    const dim3 grid((unsigned)(((long long)a.kv.units * tile + per - 1) / per), (unsigned)(to - from), 2);
     if (a.is_bf16)
-        return a.d == 64 ? cudaLaunchKernelEx(&c, window_kv_join_kernel<__nv_bfloat16, 64>, a, tile)
-                         : cudaLaunchKernelEx(&c, window_kv_join_kernel<__nv_bfloat16, 128>, a, tile);
-    return a.d == 64 ? cudaLaunchKernelEx(&c, window_kv_join_kernel<float, 64>, a, tile)
-                     : cudaLaunchKernelEx(&c, window_kv_join_kernel<float, 128>, a, tile);
+        return a.d == 64 ? launch_early(window_kv_join_kernel<__nv_bfloat16, 64>, grid, 128, 0, s, 1, a, tile)
+                         : launch_early(window_kv_join_kernel<__nv_bfloat16, 128>, grid, 128, 0, s, 1, a, tile);
+    return a.d == 64 ? launch_early(window_kv_join_kernel<float, 64>, grid, 128, 0, s, 1, a, tile)
+                     : launch_early(window_kv_join_kernel<float, 128>, grid, 128, 0, s, 1, a, tile);
 }
 
 cudaError_t window_join(const WinArgs &a, cudaStream_t s)
 {
     const long long blocks = ((long long)a.B * a.H * a.Nq + 3) / 4;
     if (a.is_bf16)
-        return a.d == 64 ? launch(window_join_kernel<__nv_bfloat16, 64>, blocks, 0, a, s, true)
-                         : launch(window_join_kernel<__nv_bfloat16, 128>, blocks, 0, a, s, true);
-    return a.d == 64 ? launch(window_join_kernel<float, 64>, blocks, 0, a, s, true)
-                     : launch(window_join_kernel<float, 128>, blocks, 0, a, s, true);
+        return a.d == 64 ? launch(window_join_kernel<__nv_bfloat16, 64>, blocks, 0, a, s)
+                         : launch(window_join_kernel<__nv_bfloat16, 128>, blocks, 0, a, s);
+    return a.d == 64 ? launch(window_join_kernel<float, 64>, blocks, 0, a, s)
+                     : launch(window_join_kernel<float, 128>, blocks, 0, a, s);
 }
 
 }  // namespace scope

@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         misc[0] = 0;
-        if (!a.counter && blockIdx.x == 0) *a.status = 0;
         bar_init(&bars->q_full, 1);
         bar_init(&bars->q_empty, 2);
         bar_init(&bars->v_land, 1);
@@ -205,8 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return it;
     };
+    early_next();
+    early_wait();
+    if (!a.counter && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     if (warp == 8 && lane == 0) fetch(0);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -581,8 +582,8 @@ cudaError_t launch_forward(WinArgs a, cudaStream_t s)
         a.counter = nullptr;   // nothing to clear first (some 2 us of a call)
     else if ((e = cudaMemsetAsync(a.status, 0, (char *)(a.counter + 1) - (char *)a.status, s)) != cudaSuccess)
         return e;
-    window_tc_kernel<D><<<(unsigned)(items < a.num_sms ? items : a.num_sms), kThreads, smem, s>>>(tq, tk, tv, a, (int)items);
-    return cudaGetLastError();
+    return launch_early(window_tc_kernel<D>, dim3((unsigned)(items < a.num_sms ? items : a.num_sms)), kThreads, smem, s, 1, tq, tk,
+                        tv, a, (int)items);
 }
 
 #undef BAR
