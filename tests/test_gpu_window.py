@@ -373,6 +373,48 @@ def test_offsets_beyond_32_bits(dtype):
     assert torch.equal(y, y0) and torch.equal(dx, d0) and torch.equal(w, w0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_calls_back_to_back_equal_calls_one_by_one(dtype):
+    """Norm, attention and gradients in one stream without a pause, over shared buffers that the next call and torch
+    overwrite, give the bits of the same calls with the device drained between them."""
+    dt, code = DT[dtype]
+    runs = [_params(dtype, H=4, Hkv=2, Nq=n, Nk=600, d=d, left=left, right=0, sinks=2, q_first=600 - n)
+            for n, d, left in ((1, 128, 500), (300, 64, 40), (1, 64, 20), (600, 128, 200), (16, 128, 599))]
+
+    def calls(pause):
+        out = []
+
+        def step(*tensors):
+            if pause:
+                torch.cuda.synchronize()
+            out.extend(t.clone() for t in tensors)
+            if pause:
+                torch.cuda.synchronize()
+
+        for p in runs:
+            Q, K, V, G = _inputs(p, dtype, 3)
+            ws = capi.alloc_window_workspace(p)
+            n = capi.QkNormParams(B=1, H=4, Hkv=4, N=p.Nq, d=p.d, d_t=p.d // 2, d_h=p.d // 4, d_w=p.d // 4, Hg=4, Wg=5,
+                                  first=0, eps=1e-6, base=10000.0, dtype=code)
+            nws, O, Y = capi.alloc_qk_norm_workspace(n), torch.empty_like(Q), torch.empty_like(Q)
+            for k in range(6):
+                capi.qk_norm_rope3d(n, Q, None, out_q=Y)
+                step()
+                _, lse = capi.window_attention(p, Y, K, V, ws=ws, out=O, lse=True)
+                step(O, lse)
+                grads = capi.window_attention_backward(p, Y, K, V, O, G, lse, ws=ws)
+                step(*grads)
+                dx, _, dw, _ = capi.qk_norm_rope3d_backward(n, Q, None, None, None, grads[0], None, ws=nws, out_q=grads[0])
+                step(dx, dw)
+                Q.mul_(1.01 if k % 2 else 0.97)   # right behind the last reader
+                K.copy_(K.flip(2))
+        torch.cuda.synchronize()
+        return out
+
+    for x, y in zip(calls(False), calls(True)):
+        assert torch.equal(x, y)
+
+
 def test_two_streams_at_once():
     """Calls with workspaces of their own, enqueued on two streams without waiting between."""
     ps = [_params("bf16", H=4, Nq=900, d=128, left=300, sinks=4), _params("bf16", H=4, Nq=1, Nk=5000, d=128, left=-1, q_first=4999)]
