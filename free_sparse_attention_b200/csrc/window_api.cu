@@ -203,8 +203,9 @@ Plan plan_of(const scope_window_params &p)
 }
 
 // Shares of the key tiles in dK, dV: a share is at most half of what a mean SM has to walk, so that
-// the few tiles that all queries see do not end last, and no shorter than 16 column tiles; in fp32,
-// whose SMs hold several blocks, half of both.  Of the shape alone.  bf16, 3 x 4 key heads x 4001,
+// the few tiles that all queries see do not end last (a quarter in fp32, whose SMs hold several
+// blocks), and no shorter than 8 column tiles (16 heads x 2000, window 300, a step: 97 us; at least 16:
+// 100).  Of the shape alone.  bf16, 3 x 4 key heads x 4001,
 // groups of 4, window 1024, 4 sinks (a tile of sinks walks 252 column tiles, the mean SM 211): 234 us
 // against 331 without shares.  fp32, 8 heads x 1430, frames of 143: 410 us against 455 with bf16's.
 KeyShares shares_of(const scope_window_params &p)
@@ -219,7 +220,7 @@ KeyShares shares_of(const scope_window_params &p)
     const long long all = (p.Nq + 63) / 64, seen = std::min(all, (std::min((left + right + 1) * p.frame, 1ll << 24) + tile + 63) / 64 + 1);
     const long long walk[2] = {G * all, G * seen};
     const long long mean = k.units * (k.sink * walk[0] + (k.tiles - k.sink) * walk[1]) / kPlanSms;
-    const long long most = p.dtype == SCOPE_BF16 ? std::max(16ll, mean / 2) : std::max(8ll, mean / 4);
+    const long long most = std::max(8ll, mean / (p.dtype == SCOPE_BF16 ? 2 : 4));
     k.of_sink = (int)((walk[0] + most - 1) / most);
     k.of_other = (int)((walk[1] + most - 1) / most);
     return k;
