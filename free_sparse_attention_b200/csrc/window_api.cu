@@ -204,10 +204,10 @@ Plan plan_of(const scope_window_params &p)
 
 // Shares of the key tiles in dK, dV: a share is at most half of what a mean SM has to walk, so that
 // the few tiles that all queries see do not end last (a quarter in fp32, whose SMs hold several
-// blocks), and no shorter than 8 column tiles (16 heads x 2000, window 300, a step: 97 us; at least 16:
-// 100).  Of the shape alone.  bf16, 3 x 4 key heads x 4001,
-// groups of 4, window 1024, 4 sinks (a tile of sinks walks 252 column tiles, the mean SM 211): 234 us
-// against 331 without shares.  fp32, 8 heads x 1430, frames of 143: 410 us against 455 with bf16's.
+// blocks), and no shorter than 8 column tiles.  Of the shape alone.  Measured: bf16, 3 x 4 key heads x
+// 4001, groups of 4, window 1024, 4 sinks (a tile of sinks walks 252 column tiles, the mean SM 211):
+// 234 us against 331 without shares; 16 heads x 2000, window 300, a step: 97 us, with shares of 16 or
+// more 100.  fp32, 8 heads x 1430, frames of 143: 410 us, with at most half 455.
 KeyShares shares_of(const scope_window_params &p)
 {
     const long long tile = p.dtype == SCOPE_BF16 ? 128 : 32, G = p.H / p.Hkv;
