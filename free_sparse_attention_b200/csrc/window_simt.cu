@@ -413,6 +413,12 @@ __global__ void __launch_bounds__(kTh) window_delta_kernel(WinArgs a)
     if (c == 0) a.delta[row] = s;
 }
 
+// A row that sees one key: P = 1 whatever the score, so dS = 0, which dP - D only meets to rounding.
+__device__ __forceinline__ bool alone(const WinRow &r)
+{
+    return r.s + r.hi - r.lo == 1;
+}
+
 // dQ: 32 query rows of one head against the key tiles they see.
 template <int D>
 __device__ __forceinline__ void dq_block(const WinArgs &a, float *sm, long long block)
@@ -452,6 +458,7 @@ __device__ __forceinline__ void dq_block(const WinArgs &a, float *sm, long long 
         const int q = r0 + ty + 8 * i;
         const bool in = q < r1;
         lim[i] = in ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
+        if (alone(lim[i])) lim[i] = WinRow{0, 0, 0};
         const long long row = win_row_index(a, b, h, in ? q : r0);
         lse[i] = in ? a.lse[row] * 1.4426950408889634f : -INFINITY;
         dl[i] = in ? a.delta[row] : 0.f;
@@ -543,12 +550,13 @@ __device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long
             const WinRow lim = in ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
             const long long row = win_row_index(a, b, h, in ? q : 0);
             const float lse = a.lse[row] * 1.4426950408889634f, dl = a.delta[row];
+            const bool lone = alone(lim);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const int key = j0 + ty + 8 * i;
                 const bool vis = key < lim.s || (key >= lim.lo && key < lim.hi);
                 s[i][j] = vis ? exp2f(fmaf(s[i][j], a.scale_log2, -lse)) : 0.f;
-                dp[i][j] = vis ? s[i][j] * (dp[i][j] - dl) : 0.f;
+                dp[i][j] = vis && !lone ? s[i][j] * (dp[i][j] - dl) : 0.f;
                 sp[(ty + 8 * i) * kLdP + tx + 16 * j] = s[i][j];
             }
         }

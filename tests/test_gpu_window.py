@@ -210,6 +210,18 @@ def test_large_logits(dtype):
     check("O", O, *ref["O"])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_query_of_one_key_has_no_gradient_of_its_scores(d):
+    """P = 1 whatever the score: dQ and dK are zeros, not what is left of two sums, and dV is dO."""
+    p = _params("f32", H=2, Nq=131, left=0, d=d)
+    Q, K, V, G = _inputs(p, "f32")
+    O, lse = capi.window_attention(p, Q, K, V, lse=True)
+    dQ, dK, dV = capi.window_attention_backward(p, Q, K, V, O, G, lse)
+    assert not dQ.any() and not dK.any()
+    # P = 2^(s c - lse log2 e): each rounding of a logit of up to |lse| is 2^-24 of it, four of them
+    assert ((dV - G).abs() <= G.abs() * (4 * 2.0 ** -24 * (1 + 2 * lse.abs()))[..., None]).all()
+
+
 def test_gradients_against_differences():
     """Central differences of the binary64 forward along random directions."""
     p = _params("f32", B=1, H=4, Hkv=2, Nq=96, d=64, left=30, right=2, sinks=2)
