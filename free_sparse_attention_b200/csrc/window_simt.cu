@@ -507,7 +507,7 @@ template <int D>
 __device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long block)
 {
     constexpr int MI = kBM / 8;
-    float *sk = sm, *sv = sk + kBM * (D + 4), *sq = sv + kBM * (D + 4), *sg = sq + kBN * (D + 4), *sp = sg + kBN * (D + 4);
+    float *sk = sm, *sv = sk + kBM * (D + 4), *sc = sv + kBM * (D + 4), *sp = sc + kBN * (D + 4);   // sc: Q, dO and Q of a tile
     const int tx = (threadIdx.x >> 1) & 15, ty = (threadIdx.x & 1) + 2 * (threadIdx.x >> 5);
     // sink blocks meet every later query: they come first in launch order
     int tile, bh, share;
@@ -529,8 +529,7 @@ __device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long
     };
     load_tile<D, kBM>(sk, kb, [&](int r) -> const float * { return j0 + r < min(j1, kl) ? kb + (j0 + r) * a.lk.n : nullptr; });
     load_tile<D, kBM>(sv, vb, [&](int r) -> const float * { return j0 + r < min(j1, kl) ? vb + (j0 + r) * a.lv.n : nullptr; });
-    queries(sg, a.G, a.lg, t0);
-    queries(sq, a.Q, a.lq, t0);
+    queries(sc, a.Q, a.lq, t0);
     uint64_t dk[MI][D / 32], dv[MI][D / 32];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -538,40 +537,50 @@ __device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long
         for (int e = 0; e < D / 32; ++e) dk[i][e] = dv[i][e] = 0ull;
     for (int t = t0; t < nt; ++t) {
         const int h = hk * G + t / per, i0 = qr.x + t % per * kBN;
-        arrived<0>();
-        float s[MI][4], dp[MI][4];
-        const Groups g = groups(0, min(4, (qr.y - i0 + 15) >> 4));
-        scores<D, MI>(s, sk, sq, ty, tx, g);
-        scores<D, MI>(dp, sv, sg, ty, tx, g);
+        float lse[4], dl[4];   // under way while the tile is
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int q = i0 + tx + 16 * j;
-            const bool in = q < qr.y;
-            const WinRow lim = in ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
-            const long long row = win_row_index(a, b, h, in ? q : 0);
-            const float lse = a.lse[row] * 1.4426950408889634f, dl = a.delta[row];
+            const long long row = win_row_index(a, b, h, q < qr.y ? q : 0);
+            lse[j] = a.lse[row];
+            dl[j] = a.delta[row];
+        }
+        arrived<0>();   // Q
+        float s[MI][4], dp[MI][4];
+        const Groups g = groups(0, min(4, (qr.y - i0 + 15) >> 4));
+        scores<D, MI>(s, sk, sc, ty, tx, g);
+        __syncthreads();
+        queries(sc, a.G, a.lg, t);
+        uint32_t some = 0;   // bit 4 i + j: the score has a gradient
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int q = i0 + tx + 16 * j;
+            const WinRow lim = q < qr.y ? win_row(a, first + q, kl) : WinRow{0, 0, 0};
+            const float nlse = lse[j] * -1.4426950408889634f;
             const bool lone = alone(lim);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const int key = j0 + ty + 8 * i;
                 const bool vis = key < lim.s || (key >= lim.lo && key < lim.hi);
-                s[i][j] = vis ? exp2f(fmaf(s[i][j], a.scale_log2, -lse)) : 0.f;
-                dp[i][j] = vis && !lone ? s[i][j] * (dp[i][j] - dl) : 0.f;
+                s[i][j] = vis ? exp2f(fmaf(s[i][j], a.scale_log2, nlse)) : 0.f;
+                some |= (uint32_t)(vis && !lone) << (4 * i + j);
                 sp[(ty + 8 * i) * kLdP + tx + 16 * j] = s[i][j];
             }
         }
-        __syncwarp();
-        accumulate<D, MI>(dv, sp, sg, ty, tx, g);
+        arrived<0>();   // dO
+        scores<D, MI>(dp, sv, sc, ty, tx, g);
+        accumulate<D, MI>(dv, sp, sc, ty, tx, g);
         __syncthreads();
-        queries(sg, a.G, a.lg, t + 1);
+        queries(sc, a.Q, a.lq, t);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sp[(ty + 8 * i) * kLdP + tx + 16 * j] = dp[i][j];
-        __syncwarp();
-        accumulate<D, MI>(dk, sp, sq, ty, tx, g);
+            for (int j = 0; j < 4; ++j)
+                sp[(ty + 8 * i) * kLdP + tx + 16 * j] = (some >> (4 * i + j)) & 1u ? s[i][j] * (dp[i][j] - dl[j]) : 0.f;
+        arrived<0>();   // Q again
+        accumulate<D, MI>(dk, sp, sc, ty, tx, g);
         __syncthreads();
-        queries(sq, a.Q, a.lq, t + 1);
+        queries(sc, a.Q, a.lq, t + 1);
     }
     arrived<0>();
     float *dkb = static_cast<float *>(a.dK) + b * a.ldk.b + hk * a.ldk.h, *dvb = static_cast<float *>(a.dV) + b * a.ldv.b + hk * a.ldv.h;
@@ -600,7 +609,7 @@ __device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long
 // Both gradients in one grid, so that the end of one kind's blocks is filled by the other's (8 heads
 // x 1430, 360 blocks of each: as two grids the busiest SM had 1.48 and 1.33 times the mean's work).
 template <int D>
-__global__ void __launch_bounds__(kTh, D == 64 ? 3 : 2) window_bwd_kernel(WinArgs a)
+__global__ void __launch_bounds__(kTh, 3) window_bwd_kernel(WinArgs a)
 {
     extern __shared__ __align__(16) float sm[];
     early_next();
@@ -642,7 +651,7 @@ cudaError_t backward(const WinArgs &a, cudaStream_t s)
     cudaError_t e = launch(window_delta_kernel<D>, (rows + kTh / 32 - 1) / (kTh / 32), 0, a, s);
     if (e != cudaSuccess) return e;
     e = launch(window_bwd_kernel<D>, a.kv.items() + (long long)a.B * a.H * ((a.Nq + kBM - 1) / kBM),
-               (2 * kBM + 2 * kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s);
+               (2 * kBM + kBN) * (D + 4) * 4 + kBM * kLdP * 4, a, s);
     return e == cudaSuccess && a.kv.parts() > 0 ? window_kv_join(a, kBM, s) : e;
 }
 
