@@ -10,10 +10,11 @@
 // (4 x 4 scores from 8 16-byte reads per 4 channels, 64 FMAs in 32 packed instructions), and rows ty + 8 i and channels
 // 4 tx + 64 j .. + 3 of an output.  Tiles arrive by cp.async as soon as their place is free (K and V
 // of a tile in turn in one place), and two to four blocks share an SM, so that one computes while
-// another waits.  Scores, softmax statistics and all sums are fp32.  Bound by the FMA pipe (82 % busy
-// on an SM with three blocks), the tiles' masked parts and the last blocks' end: the forward of 2 x 6
+// another waits (dK, dV copy Q twice a tile for the third: 389 us against 412 with two of twice the room).
+// Scores, softmax statistics and all sums are fp32.  Bound by the FMA pipe (51 to 54 % busy over all
+// SMs: 10 to 12 warps an SM do not hide the tile's barriers), the tiles' masked parts and the last blocks' end: the forward of 2 x 6
 // heads x 1777 rows, d 64, window 300, takes 81 us; 8 heads x 1430 rows, d 128, frames of 143, two before
-// and one after: forward 163 us and 9 to join, gradients 410 us, 4 for D and 7 to join.
+// and one after: forward 163 us and 9 to join, gradients 389 us, 4 for D and 7 to join.
 #include "window.cuh"
 
 namespace scope {
@@ -609,7 +610,7 @@ __device__ __forceinline__ void dkv_block(const WinArgs &a, float *sm, long long
 // Both gradients in one grid, so that the end of one kind's blocks is filled by the other's (8 heads
 // x 1430, 360 blocks of each: as two grids the busiest SM had 1.48 and 1.33 times the mean's work).
 template <int D>
-__global__ void __launch_bounds__(kTh, 3) window_bwd_kernel(WinArgs a)
+__global__ void __launch_bounds__(kTh, D == 64 ? 4 : 3) window_bwd_kernel(WinArgs a)
 {
     extern __shared__ __align__(16) float sm[];
     early_next();
