@@ -289,6 +289,45 @@ def test_captured_and_replayed_on_another_stream(Nq):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_training_step_captured_and_replayed_without_a_pause(dtype):
+    """Norm, attention with cut key tiles, and both gradients in one graph, replayed three times over before the
+    device is waited for; two graphs share the workspaces."""
+    dt, code = DT[dtype]
+    p = _params(dtype, H=4, Hkv=2, Nq=1200, d=64, left=60, sinks=4)
+    n = capi.QkNormParams(B=1, H=4, Hkv=2, N=1200, d=64, d_t=16, d_h=24, d_w=24, Hg=5, Wg=8, first=0, eps=1e-6,
+                          base=10000.0, dtype=code)
+    Q, K, V, G = _inputs(p, dtype, 50)
+    ws, nws = capi.alloc_window_workspace(p), capi.alloc_qk_norm_workspace(n)
+
+    def step():
+        Yq, Yk = capi.qk_norm_rope3d(n, Q, K)
+        O, lse = capi.window_attention(p, Yq, Yk, V, ws=ws, lse=True)
+        dYq, dYk, dV = capi.window_attention_backward(p, Yq, Yk, V, O, G, lse, ws=ws)
+        return (O, lse, dV) + capi.qk_norm_rope3d_backward(n, Q, K, None, None, dYq, dYk, ws=nws)
+
+    step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out))
+    for seed in (60, 70):
+        for t, x in zip((Q, K, V, G), _inputs(p, dtype, seed)):
+            t.copy_(x)
+        for _ in range(3):
+            for graph, _out in graphs:
+                graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        for _graph, out in graphs:
+            for x, y in zip(out, want):
+                assert torch.equal(x, y)
+
+
 def test_whole_layer_sampled_rows():
     """17550 tokens in frames of 1350, 6 of 48 heads: rows of the first, a middle and the last
     frame against the binary64 form of those rows."""
