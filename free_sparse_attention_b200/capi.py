@@ -417,8 +417,9 @@ def _refuse(fn, name, t, shape, dt, where):
 
 def _tensors(fn, p, index, layouts, named):
     """The layouts argument of a strided call (None when every tensor is dense), after a check
-    of each (name, tensor, shape): device, type, shape and contiguous channels.  A tensor of None
-    is one that the call made itself: dense, with nothing to check."""
+    of each (name, tensor, shape): device, type, shape, contiguous channels and rows that are not
+    repeated by a stride of zero.  A tensor of None is one that the call made itself: dense, with
+    nothing to check."""
     dt = torch.bfloat16 if p.dtype == SCOPE_BF16 else torch.float32
     lay = None
     for name, t, shape in named:
@@ -430,6 +431,9 @@ def _tensors(fn, p, index, layouts, named):
             st = t.stride()
             if st[3] != 1:
                 raise ValueError(f"{fn}: the channels of {name} are not contiguous (strides {st})")
+            # strides of zero mean a dense tensor to the library, and rows may not share a place
+            if any(x == 0 and n > 1 for x, n in zip(st, shape)):
+                raise ValueError(f"{fn}: the rows of {name} are repeated (strides {st}); it needs to be made contiguous")
             lay = layouts() if lay is None else lay
             setattr(lay, name, Strides(st[0], st[1], st[2]))
     return None if lay is None else ctypes.byref(lay)

@@ -410,6 +410,7 @@ scope_status scope_tc_accumulation_probe(const void *A, const void *B, int K, in
  *    heads and tokens in elements (all zero: dense [B, heads, N, d]).  A stride of a dimension
  *    longer than one is a positive multiple of 16 bytes, and no two elements share a place
  *    (else SCOPE_ERR_INVALID_ARGUMENT); elements between the rows are neither read nor written.
+ *    All zero never means one row repeated: such a tensor has to be written out first.
  *    A layouts pointer of NULL means that every tensor is dense.
  *  - Limits: d in {64, 128}; N, Nq, Nk <= 2^24; B * heads <= 2^20; B * heads * tokens < 2^31;
  *    positions of first tokens <= 2^30 (else SCOPE_ERR_UNSUPPORTED).

@@ -152,3 +152,56 @@ def test_binding_refuses_calls_off_the_gpu():
         capi.qk_norm_rope3d(q, Q, K[:, :, :30])
     with pytest.raises(ValueError):
         capi.qk_norm_rope3d_backward(q, Q, None, None, None, Q, Q, ws=ws)
+
+
+class _OnGpu(torch.Tensor):
+    """A host tensor that the binding takes for one on GPU 0."""
+
+    def get_device(self):
+        return 0
+
+
+def _on_gpu(shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype).as_subclass(_OnGpu)
+
+
+_Q, _K = (2, 4, 30, 64), (2, 2, 40, 64)
+_CALLS = {      # the tensors of each call that may have strides, in the order of its arguments
+    "norm": (lambda t: capi.qk_norm_rope3d(_norm(), t["Q"], t["K"], out_q=t["out_q"], out_k=t["out_k"]),
+             {"Q": _Q, "K": (2, 2, 30, 64), "out_q": _Q, "out_k": (2, 2, 30, 64)}),
+    "norm_backward": (lambda t: capi.qk_norm_rope3d_backward(_norm(), t["Q"], t["K"], None, None, t["dYq"], t["dYk"],
+                                                             ws=_on_gpu(1 << 20, torch.uint8), out_q=t["out_q"],
+                                                             out_k=t["out_k"]),
+                      {"Q": _Q, "K": (2, 2, 30, 64), "dYq": _Q, "dYk": (2, 2, 30, 64), "out_q": _Q,
+                       "out_k": (2, 2, 30, 64)}),
+    "window": (lambda t: capi.window_attention(_window(), t["Q"], t["K"], t["V"], ws=_on_gpu(1 << 20, torch.uint8),
+                                               out=t["out"]),
+               {"Q": _Q, "K": _K, "V": _K, "out": _Q}),
+    "window_backward": (lambda t: capi.window_attention_backward(
+        _window(), t["Q"], t["K"], t["V"], t["O"], t["dO"], _on_gpu(_Q[:3], torch.float32),
+        ws=_on_gpu(1 << 20, torch.uint8), out=(t["dQ"], t["dK"], t["dV"])),
+        {"Q": _Q, "K": _K, "V": _K, "O": _Q, "dO": _Q, "dQ": _Q, "dK": _K, "dV": _K}),
+}
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, (_, names) in _CALLS.items() for n in names])
+def test_broadcast_tensors_are_refused(L, call, name):
+    """One row expanded to a whole tensor, as the gradient of a sum is: its strides of zero are not the layout of
+    zeros that means a dense tensor.  Tensors repeated along one dimension are refused too."""
+    run, shapes = _CALLS[call]
+    shape = shapes[name]
+    for part in ((1, 1, 1, shape[3]), (1, *shape[1:]), (shape[0], 1, *shape[2:]), (*shape[:2], 1, shape[3])):
+        t = {n: _on_gpu(s) for n, s in shapes.items()}
+        t[name] = _on_gpu(part).expand(shape)
+        assert t[name].stride(3) == 1 and t[name].get_device() == 0
+        with pytest.raises(ValueError, match="repeated"):
+            run(t)
+
+
+def test_dimensions_of_one_may_have_any_stride():
+    """A stride of zero along a dimension of length one steps over nothing."""
+    p = _window(B=1, H=1, Hkv=1)
+    wide = _on_gpu((1, 30, 3, 64))[:, :, :1].transpose(1, 2)      # [1, 1, 30, 64], tokens 192 apart
+    for t in (wide, wide.as_strided((1, 1, 30, 64), (0, 0, 192, 1))):
+        lay = capi._tensors("f", p, 0, capi.WindowLayouts, (("q", t, (1, 1, 30, 64)),))._obj
+        assert lay.q.token == 192
