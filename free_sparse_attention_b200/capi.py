@@ -457,13 +457,17 @@ def _new(t, shape):
     return torch.empty_like(t) if t.shape == shape and t.is_contiguous() else t.new_empty(shape)
 
 
-def _on_stream(stream, index, made):
-    """The stream's handle; memory that the call allocated is kept for a stream of the caller's."""
+def _on_stream(stream, index, used, made):
+    """The stream's handle.  A stream of the caller's keeps the memory that the call writes, and where
+    the call allocated some (made) waits for the current stream, which may have work pending on what
+    lay there before."""
     if stream is None:
         return _raw_stream(index)
-    for t in made:
+    for t in used:
         if t is not None:
             t.record_stream(stream)
+    if made:
+        stream.wait_stream(torch.cuda.current_stream(index))
     return stream.cuda_stream
 
 
@@ -500,7 +504,7 @@ def qk_norm_rope3d(p, Q, K, w_q=None, w_k=None, first=None, out_q=None, out_k=No
     _check(fn, lib().scope_qk_norm_rope3d(
         ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, index),
         _vector(fn, "w_k", w_k, p.d, torch.float32, index), _vector(fn, "first", first, p.B, torch.int32, index),
-        Yq.data_ptr(), yp, _on_stream(stream, index, (Yq, Yk))))
+        Yq.data_ptr(), yp, _on_stream(stream, index, (Yq, Yk), out_q is None or (K is not None and out_k is None))))
     return Yq, Yk
 
 
@@ -530,7 +534,7 @@ def qk_norm_rope3d_backward(p, Q, K, w_q, w_k, dYq, dYk, first=None, ws=None, ou
         ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, index),
         _vector(fn, "w_k", w_k, p.d, torch.float32, index), dYq.data_ptr(), gp,
         _vector(fn, "first", first, p.B, torch.int32, index), dQ.data_ptr(), dp, dwq.data_ptr(), wp, ws.data_ptr(),
-        ws.numel(), _on_stream(stream, index, (ws, dQ, dK, dw))))
+        ws.numel(), _on_stream(stream, index, (ws, dQ, dK, dw), True)))
     return dQ, dK, dwq, dwk
 
 
@@ -551,6 +555,7 @@ def window_attention(p, Q, K, V, q_first=None, k_len=None, ws=None, out=None, ls
             return window_attention(p, Q, K, V, q_first, k_len, ws, out, lse, stream)
     fn, index = "scope_window_attention", Q.get_device()
     qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
+    made = ws is None or out is None or lse
     ws = alloc_window_workspace(p, Q.device) if ws is None else ws
     _workspace(fn, ws, index)
     lay = _tensors(fn, p, index, WindowLayouts, (("q", Q, qs), ("k", K, ks), ("v", V, ks), ("o", out, qs)))
@@ -560,7 +565,7 @@ def window_attention(p, Q, K, V, q_first=None, k_len=None, ws=None, out=None, ls
         ctypes.byref(p), lay, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
         _vector(fn, "q_first", q_first, p.B, torch.int32, index), _vector(fn, "k_len", k_len, p.B, torch.int32, index),
         O.data_ptr(), None if L is None else L.data_ptr(), ws.data_ptr(), ws.numel(),
-        _on_stream(stream, index, (ws, O, L))))
+        _on_stream(stream, index, (ws, O, L), made)))
     return (O, L) if lse else O
 
 
@@ -572,6 +577,7 @@ def window_attention_backward(p, Q, K, V, O, dO, lse, q_first=None, k_len=None, 
             return window_attention_backward(p, Q, K, V, O, dO, lse, q_first, k_len, ws, out, stream)
     fn, index = "scope_window_attention_backward", Q.get_device()
     qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
+    made = ws is None or out is None
     ws = alloc_window_workspace(p, Q.device) if ws is None else ws
     _workspace(fn, ws, index)
     if lse.shape != qs[:3] or lse.dtype is not torch.float32 or lse.get_device() != index or not lse.is_contiguous():
@@ -585,7 +591,7 @@ def window_attention_backward(p, Q, K, V, O, dO, lse, q_first=None, k_len=None, 
         ctypes.byref(p), lay, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), lse.data_ptr(),
         _vector(fn, "q_first", q_first, p.B, torch.int32, index), _vector(fn, "k_len", k_len, p.B, torch.int32, index),
         dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), ws.numel(),
-        _on_stream(stream, index, (ws, dQ, dK, dV))))
+        _on_stream(stream, index, (ws, dQ, dK, dV), made)))
     return dQ, dK, dV
 
 

@@ -483,6 +483,28 @@ def test_two_streams_at_once():
         assert all(torch.equal(t, y) for t in o)
 
 
+def test_outputs_made_for_another_stream_wait_for_what_lay_there():
+    """The output's memory was freed with a copy out of it still pending on the current stream."""
+    p = _params("bf16", H=4, Nq=4096, d=128, left=100)
+    Q, K, V, G = _inputs(p, "bf16", 57)
+    want, lse = capi.window_attention(p, Q, K, V, lse=True)
+    grads = capi.window_attention_backward(p, Q, K, V, want, G, lse)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        old = [torch.full_like(x, 3.0) for x in (Q, Q, K, V)]
+        kept = [torch.empty_like(x) for x in old]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(10_000_000)
+        for x, y in zip(kept, old):
+            x.copy_(y)
+        del old, x, y
+        O, L = capi.window_attention(p, Q, K, V, lse=True, stream=side)
+        got = capi.window_attention_backward(p, Q, K, V, O, G, L, stream=side)
+        torch.cuda.synchronize()
+        assert all((x == 3.0).all() for x in kept)
+        assert torch.equal(O, want) and torch.equal(L, lse) and all(torch.equal(x, y) for x, y in zip(got, grads))
+
+
 # ------------------------------------------------------------------------------ norm + RoPE
 def _norm_params(dtype, B=1, H=2, Hkv=None, N=50, split=(16, 24, 24), Hg=5, Wg=7, first=0, eps=1e-6, base=10000.0):
     return capi.QkNormParams(B=B, H=H, Hkv=Hkv or H, N=N, d=sum(split), d_t=split[0], d_h=split[1], d_w=split[2],

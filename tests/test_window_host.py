@@ -205,3 +205,51 @@ def test_dimensions_of_one_may_have_any_stride():
     for t in (wide, wide.as_strided((1, 1, 30, 64), (0, 0, 192, 1))):
         lay = capi._tensors("f", p, 0, capi.WindowLayouts, (("q", t, (1, 1, 30, 64)),))._obj
         assert lay.q.token == 192
+
+
+class _Log:
+    """Stands for a stream of the caller's, and for the library: what is done to them, in order."""
+
+    def __init__(self):
+        self.done, self.cuda_stream = [], 7
+
+    def wait_stream(self, other):
+        self.done.append(("wait", other))
+
+    def __getattr__(self, name):
+        return lambda *args: self.done.append(name) or (1 << 20 if name.endswith("_bytes") else 0)
+
+
+class _Kept(_OnGpu):
+    def record_stream(self, stream):
+        stream.done.append("kept")
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("call", ["norm", "norm_backward", "window", "window_backward"])
+def test_memory_made_for_a_stream_of_the_callers(monkeypatch, call, given):
+    """Outputs and workspaces that a call allocates come from the current stream, which may still read what lay
+    there: the caller's stream waits for it before the launch.  With buffers of the caller's there is no wait."""
+    log, t = _Log(), {n: _on_gpu(s).as_subclass(_Kept) for n, s in _CALLS[call][1].items()}
+    monkeypatch.setattr(capi, "lib", lambda: log)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index=None: ("current", index))
+    ws = torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(_Kept)
+    monkeypatch.setattr(capi, "alloc_window_workspace", lambda p, device: ws)
+    monkeypatch.setattr(capi, "alloc_qk_norm_workspace", lambda p, device: ws)
+    lse = _on_gpu(_Q[:3], torch.float32).as_subclass(_Kept)
+    own = {"ws": ws} if given else {}
+    if call == "norm":
+        own = {"out_q": t["out_q"], "out_k": t["out_k"]} if given else {"out_k": t["out_k"]}
+        capi.qk_norm_rope3d(_norm(), t["Q"], t["K"], stream=log, **own)
+    elif call == "norm_backward":
+        own = {"ws": ws, "out_q": t["out_q"], "out_k": t["out_k"]} if given else {}
+        capi.qk_norm_rope3d_backward(_norm(), t["Q"], t["K"], None, None, t["dYq"], t["dYk"], stream=log, **own)
+    elif call == "window":
+        capi.window_attention(_window(), t["Q"], t["K"], t["V"], out=t["out"], stream=log, **own)
+    else:
+        out = (t["dQ"], t["dK"], t["dV"]) if given else None
+        capi.window_attention_backward(_window(), t["Q"], t["K"], t["V"], t["O"], t["dO"], lse, out=out, stream=log, **own)
+    launch = log.done[-1]
+    assert launch.startswith("scope_") and "kept" in log.done
+    # the weights' gradients are always the call's own
+    assert (("wait", ("current", 0)) in log.done) == (not given or call == "norm_backward")
