@@ -307,12 +307,14 @@ def _exact_window(s):
 # ---------------------------------------------------------------------------------- the library's calls
 @functools.lru_cache(maxsize=64)
 def _norm_plan(B, H, Hkv, N, d_t, d_h, d_w, Hg, Wg, first, dtype):
-    """What a model keeps for its layers of one shape: the parameters and a workspace."""
+    """What a model keeps for its layers of one shape: the parameters and the workspace's size.  The
+    workspace itself comes from torch's allocator for each pass, so that passes on two streams, of
+    two threads or in two graphs have one each."""
     from free_sparse_attention_b200 import capi
     p = capi.QkNormParams(B=B, H=H, Hkv=Hkv, N=N, d=d_t + d_h + d_w, d_t=d_t, d_h=d_h, d_w=d_w, Hg=Hg, Wg=Wg,
                           first=first, eps=1e-6, base=10000.0,
                           dtype=capi.SCOPE_BF16 if dtype == "bf16" else capi.SCOPE_F32)
-    return capi, p, capi.alloc_qk_norm_workspace(p)
+    return capi, p, capi.alloc_qk_norm_workspace(p).numel()
 
 
 @functools.lru_cache(maxsize=64)
@@ -320,16 +322,17 @@ def _window_plan(B, H, Hkv, Nq, Nk, d, frame, left, right, sinks, q_first, dtype
     from free_sparse_attention_b200 import capi
     p = capi.WindowParams(B=B, H=H, Hkv=Hkv, Nq=Nq, Nk=Nk, d=d, frame=frame, left=left, right=right, sinks=sinks,
                           q_first=q_first, dtype=capi.SCOPE_BF16 if dtype == "bf16" else capi.SCOPE_F32)
-    return capi, p, capi.alloc_window_workspace(p)
+    return capi, p, capi.alloc_window_workspace(p).numel()
 
 
 def _run_norm_own(s):
     c = s["case"]
-    capi, p, ws = _norm_plan(c["B"], c["H"], c["Hkv"], c["N"], c["d_t"], c["d_h"], c["d_w"], c["Hg"], c["Wg"],
-                             c["first"], c["dtype"])
+    capi, p, size = _norm_plan(c["B"], c["H"], c["Hkv"], c["N"], c["d_t"], c["d_h"], c["d_w"], c["Hg"], c["Wg"],
+                               c["first"], c["dtype"])
     yq, yk = capi.qk_norm_rope3d(p, s["q"], s["k"], s["wq"], s["wk"], first=s["first"])
     if not c["train"]:
         return [yq, yk]
+    ws = s["q"].new_empty(size, dtype=torch.uint8)
     dq, dk, dwq, dwk = capi.qk_norm_rope3d_backward(p, s["q"], s["k"], s["wq"], s["wk"], s["gq"], s["gk"],
                                                     first=s["first"], ws=ws)
     return [yq, dq, dwq, yk, dk, dwk]
@@ -337,8 +340,9 @@ def _run_norm_own(s):
 
 def _run_window_own(s):
     c = s["case"]
-    capi, p, ws = _window_plan(c["B"], c["H"], c["Hkv"], c["Nq"], c["Nk"], c["d"], c["frame"], c["left"], c["right"],
-                               c["sinks"], c["Nk"] - c["Nq"], c["dtype"])
+    capi, p, size = _window_plan(c["B"], c["H"], c["Hkv"], c["Nq"], c["Nk"], c["d"], c["frame"], c["left"], c["right"],
+                                 c["sinks"], c["Nk"] - c["Nq"], c["dtype"])
+    ws = s["q"].new_empty(size, dtype=torch.uint8)
     at = {"q_first": s["q_first"], "k_len": s["k_len"]} if c["ragged"] else {}
     if not c["train"]:
         return [capi.window_attention(p, s["q"], s["k"], s["v"], ws=ws, **at)]
