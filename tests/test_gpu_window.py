@@ -505,6 +505,42 @@ def test_outputs_made_for_another_stream_wait_for_what_lay_there():
         assert torch.equal(O, want) and torch.equal(L, lse) and all(torch.equal(x, y) for x, y in zip(got, grads))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_entries_behind_the_first_of_a_longer_batch(dtype):
+    """Entries 1 and 2 of a batch of three by slices of everything, positions, lengths and lse too (which then start
+    4 bytes behind a multiple of 16), on the current stream and on another."""
+    p = _params(dtype, B=3, H=3, Hkv=1, Nq=35, Nk=120, left=30, right=2, sinks=2)
+    Q, K, V, G = _inputs(p, dtype, 61)
+    first, lens = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([9, 60, 85], [44, 95, 120]))
+    O, lse = capi.window_attention(p, Q, K, V, q_first=first, k_len=lens, lse=True)
+    grads = capi.window_attention_backward(p, Q, K, V, O, G, lse, q_first=first, k_len=lens)
+    rest = _params(dtype, B=2, H=3, Hkv=1, Nq=35, Nk=120, left=30, right=2, sinks=2)
+    assert first[1:].data_ptr() % 16 == 4 and lse[1:].data_ptr() % 16 == 4
+    n = capi.QkNormParams(B=3, H=3, Hkv=1, N=35, d=64, d_t=16, d_h=24, d_w=24, Hg=5, Wg=7, first=0, eps=1e-6, base=10000.0,
+                          dtype=DT[dtype][1])
+    n2 = capi.QkNormParams(B=2, H=3, Hkv=1, N=35, d=64, d_t=16, d_h=24, d_w=24, Hg=5, Wg=7, first=0, eps=1e-6, base=10000.0,
+                           dtype=DT[dtype][1])
+    w = 1 + 0.2 * _randn((65,), torch.float32, 62)
+    Y, _ = capi.qk_norm_rope3d(n, Q, None, w[1:].clone(), first=first)
+    dY, _, dw, _ = capi.qk_norm_rope3d_backward(n2, Q[1:], None, w[1:].clone(), None, G[1:], None, first=first[1:].clone())
+    torch.cuda.synchronize()
+    for stream in (None, torch.cuda.Stream()):
+        at = {"q_first": first[1:], "k_len": lens[1:], "stream": stream}
+        O2, lse2 = capi.window_attention(rest, Q[1:], K[1:], V[1:], lse=True, **at)
+        got = capi.window_attention_backward(rest, Q[1:], K[1:], V[1:], O[1:], G[1:], lse[1:], **at)
+        Y2, _ = capi.qk_norm_rope3d(n2, Q[1:], None, w[1:], first=first[1:], stream=stream)
+        dY2, _, dw2, _ = capi.qk_norm_rope3d_backward(n2, Q[1:], None, w[1:], None, G[1:], None, first=first[1:], stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(Y2, Y[1:]) and torch.equal(dY2, dY) and torch.equal(dw2, dw)
+        vis = visible(rest, [60, 85], [95, 120])
+        ref = attention(Q[1:], K[1:], V[1:], vis, G[1:])
+        check("O", O2, *ref["O"])
+        check("lse", lse2, *ref["lse"])
+        for name, x in zip(("dQ", "dK", "dV"), got):
+            check(name, x, *ref[name])
+        assert torch.equal(got[0], grads[0][1:])
+
+
 # ------------------------------------------------------------------------------ norm + RoPE
 def _norm_params(dtype, B=1, H=2, Hkv=None, N=50, split=(16, 24, 24), Hg=5, Wg=7, first=0, eps=1e-6, base=10000.0):
     return capi.QkNormParams(B=B, H=H, Hkv=Hkv or H, N=N, d=sum(split), d_t=split[0], d_h=split[1], d_w=split[2],

@@ -253,3 +253,50 @@ def test_memory_made_for_a_stream_of_the_callers(monkeypatch, call, given):
     assert launch.startswith("scope_") and "kept" in log.done
     # the weights' gradients are always the call's own
     assert (("wait", ("current", 0)) in log.done) == (not given or call == "norm_backward")
+
+
+def _off(values, dtype):
+    """A contiguous vector that starts 4 bytes behind a multiple of 16, as the rest of a longer one does."""
+    whole = torch.zeros(len(values) + 4, dtype=dtype)
+    skip = next(i for i in range(4) if (whole.data_ptr() + 4 * i) % 16 == 4)
+    t = whole[skip:skip + len(values)]
+    t.copy_(torch.tensor(values))
+    return t.as_subclass(_OnGpu)
+
+
+def test_vectors_may_start_anywhere(monkeypatch):
+    """Positions, lengths, weights and lse that are slices of longer tensors reach the library at a multiple of 16 bytes."""
+    places = {"scope_qk_norm_rope3d": {4: "w", 5: "w", 6: "first"}, "scope_window_attention": {5: "first", 6: "lens"},
+              "scope_qk_norm_rope3d_backward": {4: "w", 5: "w", 8: "first"},
+              "scope_window_attention_backward": {7: "lse", 8: "first", 9: "lens"}}
+    vectors = {"first": _off([3, 5], torch.int32), "lens": _off([11, 13], torch.int32),
+               "w": _off([0.5 * i for i in range(64)], torch.float32), "lse": _off([0.1 * i for i in range(240)], torch.float32)}
+    called = []
+
+    class Library:
+        def __getattr__(self, name):
+            def f(*args):
+                for i, what in places.get(name, {}).items():
+                    assert args[i] % 16 == 0, (name, what)
+                    want = vectors[what]
+                    got = (ctypes.c_uint8 * (4 * want.numel())).from_address(args[i])
+                    assert bytes(got) == want.as_subclass(torch.Tensor).numpy().tobytes(), (name, what)
+                called.append(name)
+                return 0
+            return f
+
+    monkeypatch.setattr(capi, "lib", lambda: Library())
+    monkeypatch.setattr(capi, "_raw_stream", lambda index: 0)
+    first, lens, w, lse = (vectors[n] for n in ("first", "lens", "w", "lse"))
+    ws = _on_gpu(1 << 20, torch.uint8)
+    t = {call: {n: _on_gpu(s) for n, s in shapes.items()} for call, (_, shapes) in _CALLS.items()}
+    x = t["norm"]
+    capi.qk_norm_rope3d(_norm(), x["Q"], x["K"], w, w, first=first)
+    x = t["norm_backward"]
+    capi.qk_norm_rope3d_backward(_norm(), x["Q"], x["K"], w, w, x["dYq"], x["dYk"], first=first, ws=ws)
+    x = t["window"]
+    capi.window_attention(_window(), x["Q"], x["K"], x["V"], q_first=first, k_len=lens, ws=ws)
+    x = t["window_backward"]
+    capi.window_attention_backward(_window(), x["Q"], x["K"], x["V"], x["O"], x["dO"], lse.view(_Q[:3]), q_first=first,
+                                   k_len=lens, ws=ws)
+    assert sorted(called) == sorted(places)
