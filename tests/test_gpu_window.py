@@ -210,6 +210,39 @@ def test_large_logits(dtype):
     check("O", O, *ref["O"])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients_of_large_logits(d, dtype):
+    """The same logits of hundreds in the gradients, where P is 2^(c s - lse log2 e), the difference of two large numbers."""
+    p = _params(dtype, Nq=140, Nk=600, d=d, left=-1, right=-1)
+    Q, K, V, G = _inputs(p, dtype, 13)
+    K = K + (torch.arange(600, device="cuda") / 25.0)[:, None].to(K.dtype) * Q[:, :, :1].sign()
+    Q = Q.abs() * Q[:, :, :1].sign()
+    ref = attention(Q, K, V, visible(p, [0], [600]), G)
+    O, lse = capi.window_attention(p, Q, K, V, lse=True)
+    assert 200 < lse.abs().max() < 2000
+    check("O", O, *ref["O"])
+    check("lse", lse, *ref["lse"])
+    grads = capi.window_attention_backward(p, Q, K, V, O, G, lse)
+    # The bounds above are relative.  Here most P are below 2^-126 (the logits span hundreds, 2^-126 is e^-87), the least
+    # normal number, under which an exponential, a product or an operand may be flushed to 0: off by at most 2^-126 each.
+    # P and dS = P (dP - D) are then off by 2^-126 and 2^-126 (|dP| + |D| + 1), the sums by that times the other factor,
+    # and a result by 2^-126.
+    tiny, sc = 2.0 ** -126, 1.0 / math.sqrt(d)
+    q, k, v, g = (x.double() for x in (Q, K, V, G))
+    ds = tiny * ((g @ v.mT).abs() + (g * ref["O"][0]).sum(-1, keepdim=True).abs() + 1)
+    under = {"dQ": sc * ds @ k.abs() + tiny, "dK": sc * ds.mT @ q.abs() + tiny, "dV": tiny * (g.abs().sum(2, keepdim=True) + 1)}
+    for n, t in zip(("dQ", "dK", "dV"), grads):
+        check(n, t, ref[n][0], ref[n][1] + under[n])
+    # sum_j P_ij = 1, so the keys' dV add up to the queries' dO whatever the logits.  A logit and lse meet in both
+    # passes with the same bits: four roundings of up to |lse| and one each of 600 and 64 terms of the row sum, in
+    # binary32; of the sums over 140 queries as many; half a step of bf16 on P and on every dV
+    low = 2.0 ** -8 if dtype == "bf16" else 0.0
+    u = low + 2.0 ** -24 * (4 * (1 + 2 * lse.double().abs()) + 664 + 204)
+    bound = 1.02 * (G.double().abs() * u[..., None]).sum(2) + low * grads[2].double().abs().sum(2)
+    assert ((grads[2].double().sum(2) - G.double().sum(2)).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_query_of_one_key_has_no_gradient_of_its_scores(d):
     """P = 1 whatever the score: dQ and dK are zeros, not what is left of two sums, and dV is dO."""
