@@ -78,3 +78,10 @@ def test_attention_traffic_record_follows_the_kernel_source(tmp_path):
     changed = tmp_path / "attention_tc.cu"
     changed.write_bytes(body + b"\n")
     assert bench.traffic_from_profile(str(changed)) is None
+
+
+def test_the_attention_traffic_record_is_of_the_current_source():
+    """The bench line has its DRAM traffic: the counters were captured from the kernel's source as it is."""
+    import bench
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    assert bench.traffic_from_profile(os.path.join(root, "free_sparse_attention_b200", "csrc", "attention_tc.cu"))
