@@ -106,6 +106,30 @@ scope_status validate(const scope_qk_norm_params *p)
     return SCOPE_OK;
 }
 
+// Turns per position of an axis of n pairs: r^i / 2 pi with r = base^(-1 / n), into f[k ..]; returns
+// the end.  r's error comes back i times in r^i, so r is corrected by one Newton step of r^n = 1 / base
+// and all powers are taken in long double (64 bits of mantissa): a frequency is rounded to binary64 once.
+// (A long double pow for each axis takes 1.3 us of a call, this 0.15.)
+int axis_frequencies(double base, int n, double *f, int k)
+{
+    if (n == 0) return k;
+    const double r0 = std::pow(base, -1.0 / n);
+    long double power = 1.0L, square = r0;
+    for (int e = n; e; e >>= 1) {
+        if (e & 1) power *= square;
+        square *= square;
+    }
+    const long double r = r0 * (1.0L - (base * power - 1.0L) / n), rr = r * r;
+    long double even = 0.159154943091895335768883763372514362L, odd = even * r;   // two chains side by side
+    for (int i = 0; i < n; i += 2) {
+        f[k++] = (double)even;
+        if (i + 1 < n) f[k++] = (double)odd;
+        even *= rr;
+        odd *= rr;
+    }
+    return k;
+}
+
 scope_status norm_args(const scope_qk_norm_params &p, const int32_t *first, NormArgs &a)
 {
     a.B = p.B;
@@ -121,16 +145,8 @@ scope_status norm_args(const scope_qk_norm_params &p, const int32_t *first, Norm
     a.first = first;
     a.first0 = p.first;
     a.eps = (float)p.eps;
-    // turns per position of pair i of an axis: r^i / 2 pi, r = base^(-2 / width), by squares (a
-    // handful of roundings each)
     int k = 0;
-    for (int w : {p.d_t, p.d_h, p.d_w}) {
-        double *f = a.freq + k;
-        const double r = w ? std::pow(p.base, -2.0 / w) : 1.0;
-        for (int i = 0; i < w / 2; ++i) f[i] = i == 0 ? 1.0 : (i & 1 ? f[i - 1] * r : f[i / 2] * f[i / 2]);
-        k += w / 2;
-    }
-    for (int i = 0; i < k; ++i) a.freq[i] *= 0.15915494309189535;
+    for (int w : {p.d_t, p.d_h, p.d_w}) k = axis_frequencies(p.base, w / 2, a.freq, k);
     return SCOPE_OK;
 }
 

@@ -619,6 +619,32 @@ def test_qk_norm_rope3d_and_gradients(shape, dtype):
     check("dw", w1, *ref["dw"])
 
 
+@pytest.mark.parametrize("base", [10000.0, 100.0, 1.5, 0.5])
+def test_qk_norm_rope3d_angles_of_the_farthest_positions(base):
+    """Pairs (1, 0) turned by the angles of positions 2^30 and on, against angles of 40 digits.
+    The frequency and its product with the position are each half a step of binary64 off, 2^-53 of at most 1.98 x 2^30
+    radians (base 0.5, the last pair): 8 x 2^-24 in all, and 1 for the frequency's own arithmetic.  The rest is reduced to a turn, so its rounding to binary32
+    is at most pi 2^-25, and cos and sin are within 2 units of 2^-24: 13 x 2^-24.  The mean of 128 squares of 0 and 1 is
+    exact; eps, the root, and three products or sums take 5 steps of y = 2^(1/2) cos or sin."""
+    import decimal
+    D = decimal.Decimal
+    p = _norm_params("f32", B=1, H=1, N=8, split=(128, 0, 0), Hg=1, Wg=1, first=1 << 30, base=base)
+    Q = torch.zeros((1, 1, 8, 128), device="cuda")
+    Q[..., 0::2] = 1
+    Y, _ = capi.qk_norm_rope3d(p, Q, None)
+    pi = D("3.1415926535897932384626433832795028841971693993751")
+    want = torch.empty((8, 128), dtype=torch.float64)
+    with decimal.localcontext() as c:
+        c.prec = 40
+        for i in range(64):
+            f = (D(base).ln() * -2 * i / 128).exp()
+            for n in range(8):
+                a = float((((1 << 30) + n) * f) % (2 * pi))
+                want[n, 2 * i], want[n, 2 * i + 1] = math.cos(a), math.sin(a)
+    want *= 1 / math.sqrt(0.5 + 1e-6)
+    assert (Y[0, 0].double().cpu() - want).abs().max() <= 18 * 2.0 ** -24 * math.sqrt(2)
+
+
 def test_qk_norm_rope3d_rows_of_zeros():
     p = _norm_params("f32", N=9)
     Q = torch.zeros((1, 2, 9, 64), device="cuda")
