@@ -439,21 +439,21 @@ def _tensors(fn, p, index, layouts, named):
     return None if lay is None else ctypes.byref(lay)
 
 
-def _vector(fn, name, t, n, dtype, index, stream=None, kept=None):
+def _vector(fn, name, t, n, dtype, index, on=None):
     """The address of a vector argument, after its checks."""
     if t is None:
         return None
     if t.shape != (n,) or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
         _refuse(fn, name, t, (n,), dtype, f"cuda:{index}")
-    return _place(t, stream, kept)
-
-
-def _place(t, stream, kept):
-    """t's address, or that of a copy at a multiple of 16 bytes, as the library wants it (t may be a
-    slice of a longer tensor).  The copy is made on the call's stream, and `kept` until the launch."""
     at = t.data_ptr()
-    if at % 16 == 0:
-        return at
+    return _copied(t, on) if at & 15 else at
+
+
+def _copied(t, on):
+    """The address of a copy of t at a multiple of 16 bytes, as the library wants it (t may be a slice
+    of a longer tensor).  on: the call's stream, where the copy is made, and what it keeps until its
+    launch."""
+    stream, kept = on
     if stream is None:
         t = t.clone()
     else:
@@ -474,11 +474,9 @@ def _new(t, shape):
 
 
 def _on_stream(stream, index, used, made):
-    """The stream's handle.  A stream of the caller's keeps the memory that the call writes, and where
-    the call allocated some (made) waits for the current stream, which may have work pending on what
-    lay there before."""
-    if stream is None:
-        return _raw_stream(index)
+    """The handle of a stream of the caller's.  It keeps the memory that the call writes, and where the
+    call allocated some (made) waits for the current stream, which may have work pending on what lay
+    there before."""
     for t in used:
         if t is not None:
             t.record_stream(stream)
@@ -508,7 +506,7 @@ def qk_norm_rope3d(p, Q, K, w_q=None, w_k=None, first=None, out_q=None, out_k=No
         with torch.cuda.device(Q.device):
             return qk_norm_rope3d(p, Q, K, w_q, w_k, first, out_q, out_k, stream)
     fn, index, qs = "scope_qk_norm_rope3d", Q.get_device(), (p.B, p.H, p.N, p.d)
-    on = index, stream, []
+    on = stream, []
     if K is None:
         Yk = kp = yp = None
         lay = _tensors(fn, p, index, QkNormLayouts, (("q", Q, qs), ("yq", out_q, qs)))
@@ -519,9 +517,11 @@ def qk_norm_rope3d(p, Q, K, w_q=None, w_k=None, first=None, out_q=None, out_k=No
         kp, yp = K.data_ptr(), Yk.data_ptr()
     Yq = _new(Q, qs) if out_q is None else out_q
     _check(fn, lib().scope_qk_norm_rope3d(
-        ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, *on),
-        _vector(fn, "w_k", w_k, p.d, torch.float32, *on), _vector(fn, "first", first, p.B, torch.int32, *on),
-        Yq.data_ptr(), yp, _on_stream(stream, index, (Yq, Yk), out_q is None or (K is not None and out_k is None))))
+        ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, index, on),
+        _vector(fn, "w_k", w_k, p.d, torch.float32, index, on),
+        _vector(fn, "first", first, p.B, torch.int32, index, on),
+        Yq.data_ptr(), yp, _raw_stream(index) if stream is None else
+        _on_stream(stream, index, (Yq, Yk), out_q is None or (K is not None and out_k is None))))
     return Yq, Yk
 
 
@@ -532,7 +532,7 @@ def qk_norm_rope3d_backward(p, Q, K, w_q, w_k, dYq, dYk, first=None, ws=None, ou
         with torch.cuda.device(Q.device):
             return qk_norm_rope3d_backward(p, Q, K, w_q, w_k, dYq, dYk, first, ws, out_q, out_k, stream)
     fn, index, qs = "scope_qk_norm_rope3d_backward", Q.get_device(), (p.B, p.H, p.N, p.d)
-    on = index, stream, []
+    on = stream, []
     if (K is None) != (dYk is None):
         raise ValueError(f"{fn}: K and dYk go together")
     ws = alloc_qk_norm_workspace(p, Q.device) if ws is None else ws
@@ -549,10 +549,10 @@ def qk_norm_rope3d_backward(p, Q, K, w_q, w_k, dYq, dYk, first=None, ws=None, ou
         dK, dwk = _new(K, ks) if out_k is None else out_k, dw[1]
         kp, gp, dp, wp = K.data_ptr(), dYk.data_ptr(), dK.data_ptr(), dwk.data_ptr()
     _check(fn, lib().scope_qk_norm_rope3d_backward(
-        ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, *on),
-        _vector(fn, "w_k", w_k, p.d, torch.float32, *on), dYq.data_ptr(), gp,
-        _vector(fn, "first", first, p.B, torch.int32, *on), dQ.data_ptr(), dp, dwq.data_ptr(), wp, ws.data_ptr(),
-        ws.numel(), _on_stream(stream, index, (ws, dQ, dK, dw), True)))
+        ctypes.byref(p), lay, Q.data_ptr(), kp, _vector(fn, "w_q", w_q, p.d, torch.float32, index, on),
+        _vector(fn, "w_k", w_k, p.d, torch.float32, index, on), dYq.data_ptr(), gp,
+        _vector(fn, "first", first, p.B, torch.int32, index, on), dQ.data_ptr(), dp, dwq.data_ptr(), wp, ws.data_ptr(),
+        ws.numel(), _raw_stream(index) if stream is None else _on_stream(stream, index, (ws, dQ, dK, dw), True)))
     return dQ, dK, dwq, dwk
 
 
@@ -572,7 +572,7 @@ def window_attention(p, Q, K, V, q_first=None, k_len=None, ws=None, out=None, ls
         with torch.cuda.device(Q.device):
             return window_attention(p, Q, K, V, q_first, k_len, ws, out, lse, stream)
     fn, index = "scope_window_attention", Q.get_device()
-    on = index, stream, []
+    on = stream, []
     qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
     made = ws is None or out is None or lse
     ws = alloc_window_workspace(p, Q.device) if ws is None else ws
@@ -582,9 +582,10 @@ def window_attention(p, Q, K, V, q_first=None, k_len=None, ws=None, out=None, ls
     L = Q.new_empty(qs[:3], dtype=torch.float32) if lse else None
     _check(fn, lib().scope_window_attention(
         ctypes.byref(p), lay, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
-        _vector(fn, "q_first", q_first, p.B, torch.int32, *on), _vector(fn, "k_len", k_len, p.B, torch.int32, *on),
+        _vector(fn, "q_first", q_first, p.B, torch.int32, index, on),
+        _vector(fn, "k_len", k_len, p.B, torch.int32, index, on),
         O.data_ptr(), None if L is None else L.data_ptr(), ws.data_ptr(), ws.numel(),
-        _on_stream(stream, index, (ws, O, L), made)))
+        _raw_stream(index) if stream is None else _on_stream(stream, index, (ws, O, L), made)))
     return (O, L) if lse else O
 
 
@@ -595,7 +596,7 @@ def window_attention_backward(p, Q, K, V, O, dO, lse, q_first=None, k_len=None, 
         with torch.cuda.device(Q.device):
             return window_attention_backward(p, Q, K, V, O, dO, lse, q_first, k_len, ws, out, stream)
     fn, index = "scope_window_attention_backward", Q.get_device()
-    on = index, stream, []
+    on = stream, []
     qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.Hkv, p.Nk, p.d)
     made = ws is None or out is None
     ws = alloc_window_workspace(p, Q.device) if ws is None else ws
@@ -608,10 +609,12 @@ def window_attention_backward(p, Q, K, V, O, dO, lse, q_first=None, k_len=None, 
     if out is None:
         dQ, dK, dV = _new(Q, qs), _new(K, ks), _new(V, ks)
     _check(fn, lib().scope_window_attention_backward(
-        ctypes.byref(p), lay, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), _place(lse, *on[1:]),
-        _vector(fn, "q_first", q_first, p.B, torch.int32, *on), _vector(fn, "k_len", k_len, p.B, torch.int32, *on),
+        ctypes.byref(p), lay, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(),
+        _copied(lse, on) if lse.data_ptr() & 15 else lse.data_ptr(),
+        _vector(fn, "q_first", q_first, p.B, torch.int32, index, on),
+        _vector(fn, "k_len", k_len, p.B, torch.int32, index, on),
         dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), ws.numel(),
-        _on_stream(stream, index, (ws, dQ, dK, dV), made)))
+        _raw_stream(index) if stream is None else _on_stream(stream, index, (ws, dQ, dK, dV), made)))
     return dQ, dK, dV
 
 
