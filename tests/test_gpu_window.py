@@ -361,6 +361,75 @@ def test_training_step_captured_and_replayed_without_a_pause(dtype):
                 assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_captured_with_more_items_than_multiprocessors(d):
+    """A forward of 200 items of 256 rows, whose counter is cleared by a node of its own in the graph."""
+    p = _params("bf16", H=40, Hkv=8, Nq=1200, d=d, left=150, sinks=2)
+    Q, K, V, G = _inputs(p, "bf16", 71)
+    ws = capi.alloc_window_workspace(p)
+
+    def step():
+        O, lse = capi.window_attention(p, Q, K, V, ws=ws, lse=True)
+        return (O, lse) + capi.window_attention_backward(p, Q, K, V, O, G, lse, ws=ws)
+
+    want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert capi.get_device_status(ws) == 0
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("over", [dict(frame=1 << 24, left=1 << 30, right=1 << 30, sinks=1 << 30),
+                                  dict(frame=1, left=0, right=1 << 30, sinks=1 << 30), dict(frame=1 << 24, left=0, right=0),
+                                  dict(frame=3, left=1 << 30, right=0, q_first=(1 << 30) - 3),
+                                  dict(frame=2, left=0, right=0, sinks=1, q_first=1 << 30)])
+def test_windows_at_the_limits_of_their_numbers(over, dtype):
+    """Limits of windows, frames and positions, whose products take 55 bits."""
+    _run(_params(dtype, Nq=70, Nk=150, **{"left": 5, **over}), dtype)
+
+
+def test_two_threads_at_once():
+    """Two host threads, each on a stream of its own with default workspaces and outputs."""
+    import threading
+    ps = [_params("bf16", H=4, Hkv=2, Nq=700, d=128, left=200, sinks=4), _params("f32", H=2, Nq=400, left=90, sinks=1)]
+    ins = [_inputs(p, t, 81) for p, t in zip(ps, ("bf16", "f32"))]
+
+    def step(p, x):
+        O, lse = capi.window_attention(p, *x[:3], lse=True)
+        return (O, lse) + capi.window_attention_backward(p, *x[:3], O, x[3], lse)
+
+    want = [step(p, x) for p, x in zip(ps, ins)]
+    torch.cuda.synchronize()
+    got, failed = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i].append(step(ps[i], ins[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for w, runs in zip(want, got):
+        assert len(runs) == 20 and all(torch.equal(x, y) for out in runs for x, y in zip(out, w))
+
+
 def test_whole_layer_sampled_rows():
     """17550 tokens in frames of 1350, 6 of 48 heads: rows of the first, a middle and the last
     frame against the binary64 form of those rows."""
