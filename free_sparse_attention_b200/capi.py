@@ -501,7 +501,8 @@ def qk_norm_rope3d(p, Q, K, w_q=None, w_k=None, first=None, out_q=None, out_k=No
     """RMS norm per head with a weight per channel, and 3D RoPE, of Q [B,H,N,d] and K
     [B,Hkv,N,d] (K may be None) in one pass.  Strided tensors are taken as they are; out_q /
     out_k may be Q / K.  first: int32 [B] positions of the entries' first tokens (default
-    p.first).  Returns (Yq, Yk)."""
+    p.first).  Returns (Yq, Yk).  Nothing is recorded for autograd: gradients come from
+    qk_norm_rope3d_backward."""
     if _elsewhere(Q):
         with torch.cuda.device(Q.device):
             return qk_norm_rope3d(p, Q, K, w_q, w_k, first, out_q, out_k, stream)
@@ -567,7 +568,8 @@ def window_attention(p, Q, K, V, q_first=None, k_len=None, ws=None, out=None, ls
     """Attention of Q [B,H,Nq,d] over the keys K, V [B,Hkv,Nk,d] inside each query's window of
     frames, and the first p.sinks frames.  q_first, k_len: int32 [B] position of each entry's
     first query and its number of keys (default p.q_first and Nk).  Returns O, or (O, lse
-    [B,H,Nq] float32) with lse=True, which window_attention_backward needs."""
+    [B,H,Nq] float32) with lse=True, which window_attention_backward needs.  Nothing is recorded for
+    autograd."""
     if _elsewhere(Q):
         with torch.cuda.device(Q.device):
             return window_attention(p, Q, K, V, q_first, k_len, ws, out, lse, stream)

@@ -191,7 +191,8 @@ Plan plan_of(const scope_window_params &p)
     for (int n = 2; r.few && n <= G && n * p.Nq <= 16; ++n)
         if (G % n == 0) r.pack = n;
     // rows of one item and keys of one of its tiles: few rows, tensor cores, or fp32; items
-    // that the device holds at a time
+    // that the plan takes the device to hold at a time (fp32 at d 128: two an SM, where the kernel has
+    // come to fit three; three here is not measured)
     const bool bf16 = p.dtype == SCOPE_BF16;
     const int bm = r.few ? 16 : (bf16 ? 256 : 32), bn = r.few && bf16 ? 16 : 64;
     const int slots = kPlanSms * (bf16 ? (r.few ? 2 : 1) : (p.d == 64 ? 4 : 2));

@@ -9,11 +9,11 @@
 // rows meet different banks.  A thread owns rows ty + 8 i and columns tx + 16 j of a score tile
 // (4 x 4 scores from 8 16-byte reads per 4 channels, 64 FMAs in 32 packed instructions), and rows ty + 8 i and channels
 // 4 tx + 64 j .. + 3 of an output.  Tiles arrive by cp.async as soon as their place is free (K and V
-// of a tile in turn in one place), and two to four blocks share an SM, so that one computes while
+// of a tile in turn in one place), and three blocks (d 128) or four (d 64) share an SM, so that one computes while
 // another waits (dK, dV copy Q twice a tile for the third: 389 us against 412 with two of twice the room).
 // Scores, softmax statistics and all sums are fp32.  Bound by the FMA pipe (51 to 58 % busy over all
 // SMs: 10 to 12 warps an SM do not hide the tile's barriers), the tiles' masked parts and the last blocks' end: the forward of 2 x 6
-// heads x 1777 rows, d 64, window 300, takes 81 us; 8 heads x 1430 rows, d 128, frames of 143, two before
+// heads x 1777 rows, d 64, window 300, takes 78 us; 8 heads x 1430 rows, d 128, frames of 143, two before
 // and one after: forward 163 us and 9 to join, gradients 389 us, 4 for D and 7 to join.
 #include "window.cuh"
 
